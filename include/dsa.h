@@ -297,6 +297,106 @@ dsa_status dsa_sparse_mla_decode_fp8(const void* q, const void* kv_pool, float k
                                      size_t ws_bytes, void* stream);
 
 /*
+ * Appending tokens to the paged latent cache, with the position rotation
+ * applied on the way  (section 2.1: one cached latent per token, 512 kv-rank
+ * values and a 64-d RoPE part; the pages give no call for it).  Row t of
+ * sequence b (q_offsets, as above) is the token at position q_vis[t] - 1, the
+ * position from which that row's query then sees itself, so one decode step
+ * hands the same q_offsets and q_vis to this call and to the attention.
+ *   kv         bf16 [T,512], rows ld_kv elements apart (ld_kv >= 512, a
+ *              multiple of 8): the (normalised) latents
+ *   k_pe       bf16 [T,64], rows ld_pe elements apart (ld_pe >= 64, even;
+ *              4-byte aligned): the RoPE parts before rotation
+ *   inv_freq   fp32 [32]: angle of pair i = position * inv_freq[i], reduced
+ *              in 64 bits, so far positions keep their angle
+ *   interleaved  0: pairs (i, i + 32); else pairs (2i, 2i + 1).  A pair (x, y)
+ *              becomes (x cos - y sin, y cos + x sin)
+ *   kv_pool    the cache, page_table as in dsa_sparse_mla_decode:
+ *              kv_scales NULL:  bf16 [num_pages,page_size,576]
+ *              else             e4m3 [num_pages,page_size,576], and
+ *   kv_scales  fp32 [num_pages, page_size/scale_block]: one scale for each
+ *              block of scale_block tokens (a power of two, at most page_size)
+ * Each value is rounded once, from fp32 (a bf16 cache keeps the latents as
+ * they are).  A block's scale is 2^e, e the smallest in [-40, 40] with
+ * amax <= 448 * 2^e over its finite values; values beyond saturate, NaN and
+ * infinities are stored as NaN.  A block that holds tokens already (the
+ * positions before the first new one) keeps its scale or takes the larger one
+ * the new tokens need, and its codes are then rescaled by old / new and
+ * rounded again.  A block whose first position is appended starts afresh.
+ * The rows of a sequence are consecutive positions.  A row with q_vis = 0 is
+ * padding and is skipped, the first row of a sequence only where all are; any
+ * other row that breaks the order, and a position without a valid page, is
+ * skipped and flagged (DSA_ERR_DEVICE_BOUNDS), as is a partly filled block's
+ * old scale outside [2^-40, 2^40] (its codes are left as they are).  Rows
+ * outside every sequence, and cache rows of other positions, stay as they
+ * were.  A page that is appended to belongs to one sequence of the call.
+ * B <= DSA_MAX_BATCH; T, and the rows of a sequence, are not limited.
+ * ws: at least 256 bytes (the error word).
+ */
+dsa_status dsa_latent_append(const void* kv, int64_t ld_kv, const void* k_pe, int64_t ld_pe,
+                             const float* inv_freq, int interleaved, const int32_t* page_table,
+                             int max_pages, const int32_t* q_offsets, const int32_t* q_vis, int B,
+                             int T, void* kv_pool, float* kv_scales, int num_pages, int page_size,
+                             int scale_block, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Bytes of device workspace that dsa_mla_decode_sinks and
+ * dsa_sparse_mla_decode_fp8_block need: the error word and the partial
+ * results of queries whose tokens are divided over several SM pairs.  It
+ * depends on the heads alone; zeroed once before its first use, reused by
+ * consecutive calls on one stream.  Returns 0 for a head count that is not
+ * 128 or 64.
+ */
+size_t dsa_attend_workspace_bytes(int heads);
+
+/*
+ * MLA decode over a sliding window and a few first tokens that stay visible
+ * (sinks): query q attends, in one softmax, to the positions s < q_vis[q] with
+ * s < sinks or s >= q_vis[q] - window.  window >= the context is dense
+ * attention; an empty set gives O = 0, LSE = -inf.  The pages have no
+ * counterpart of the sinks; it serves dense and windowed layers over the cache
+ * that dsa_latent_append writes.
+ *   q          bf16 [Q,heads,576] absorbed queries, heads = 128 or 64
+ *   kv_pool, kv_scales, scale_block, page_table: the cache, as in
+ *              dsa_latent_append (kv_scales NULL: bf16); every scale in
+ *              [2^-40, 2^40], powers of two or not
+ *   sinks, window  >= 0
+ *   out        bf16 [Q,heads,512]    lse fp32 [Q,heads] (natural log)
+ * Any number of queries per sequence (Q <= 65535).  Positions without a valid
+ * page, or whose scale is out of its range, are skipped and flagged
+ * (DSA_ERR_DEVICE_BOUNDS), as is a q_vis beyond max_pages * page_size.  Cache
+ * rows that the set does not hold are not read.
+ * Precision: products accumulate in fp32 on the tensor cores; scores, maxima
+ * and sums are fp32.  Over a bf16 cache the softmax weights are rounded to
+ * bf16 for the value product; over an e4m3 cache weights, codes and queries
+ * are fp16 there (codes exactly; queries after scaling each head by a power of
+ * two, exact except for elements 2^-28 times smaller than the head's largest).
+ * ws: at least dsa_attend_workspace_bytes(heads) bytes, 16-byte aligned.
+ */
+dsa_status dsa_mla_decode_sinks(const void* q, const void* kv_pool, const float* kv_scales,
+                                int num_pages, int page_size, int scale_block,
+                                const int32_t* page_table, int max_pages, const int32_t* q_offsets,
+                                const int32_t* q_vis, int B, int Q, int heads, int sinks,
+                                int window, float scale, void* out, float* lse, void* ws,
+                                size_t ws_bytes, void* stream);
+
+/*
+ * Sparse MLA decode over an e4m3 latent cache with one scale for each block of
+ * tokens (dsa_sparse_mla_decode_fp8 has one for the whole cache): the selected
+ * positions idx int32 [Q,topk] (any order, -1 = skip) of the cache that
+ * dsa_latent_append writes.  Entries with idx >= q_vis[q] or idx < -1 are skipped and
+ * flagged.  Other arguments, output types, precision and errors as in
+ * dsa_mla_decode_sinks; topk <= DSA_MAX_TOPK.
+ */
+dsa_status dsa_sparse_mla_decode_fp8_block(const void* q, const void* kv_pool,
+                                           const float* kv_scales, int num_pages, int page_size,
+                                           int scale_block, const int32_t* page_table,
+                                           int max_pages, const int32_t* q_offsets,
+                                           const int32_t* q_vis, const int32_t* idx, int B, int Q,
+                                           int heads, int topk, float scale, void* out, float* lse,
+                                           void* ws, size_t ws_bytes, void* stream);
+
+/*
  * Sparse MLA decode that allocates nothing and takes no workspace.  The
  * pages have no counterpart of this call; it exists for callers that cannot
  * hand the library device memory: a serving engine whose allocator already

@@ -53,6 +53,13 @@ SIGNATURES = {
                                           _I, _I, _I, _F, _I, _P, _P, _P, _SZ, _P]),
     "dsa_sparse_mla_decode_fp8": (_I, [_P, _P, _F, _I, _I, _P, _I, _P, _P, _P, _I, _I, _I, _I, _F,
                                        _I, _P, _P, _P, _SZ, _P]),
+    "dsa_latent_append": (_I, [_P, _I64, _P, _I64, _P, _I, _P, _I, _P, _P, _I, _I, _P, _P, _I, _I,
+                               _I, _P, _SZ, _P]),
+    "dsa_attend_workspace_bytes": (_SZ, [_I]),
+    "dsa_mla_decode_sinks": (_I, [_P, _P, _P, _I, _I, _I, _P, _I, _P, _P, _I, _I, _I, _I, _I, _F,
+                                  _P, _P, _P, _SZ, _P]),
+    "dsa_sparse_mla_decode_fp8_block": (_I, [_P, _P, _P, _I, _I, _I, _P, _I, _P, _P, _P, _I, _I, _I,
+                                             _I, _F, _P, _P, _P, _SZ, _P]),
     "dsa_lse_combine": (_I, [_P, _P, _I, _I, _I, _P, _P, _P]),
     "dsa_decode_step": (_I, [_I, _I, _I, _PP, _PP, _PP, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                              _PP, _PP, _I, _I, _PP, _I, _F, _I, _PP, _PP, _P, _P, _SZ, _P]),
@@ -241,6 +248,112 @@ def dsa_sparse_mla_decode_fp8(q, kv_pool, kv_scale, page_table, q_offsets, q_vis
         _ptr(page_table), page_table.shape[1], _ptr(q_offsets), _ptr(q_vis), _ptr(idx), B,
         q.shape[0], q.shape[1], idx.shape[1], float(scale), num_splits, _ptr(out), _ptr(lse),
         _ptr(ws), ws.numel(), _stream(stream)), "dsa_sparse_mla_decode_fp8")
+
+
+def _rows_ptr(t: torch.Tensor, width: int, dtype, name: str):
+    """Pointer of a [T, width] device tensor whose rows may be apart."""
+    if not t.is_cuda:
+        raise ValueError("libdsa takes device tensors")
+    if t.dtype != dtype or t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
+        raise ValueError(f"{name}: [T, {width}] {dtype} with dense rows")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _expect(name: str, t: torch.Tensor, dtype, *shape):
+    """Type and shape (None: any) of a tensor, on the current device."""
+    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
+    if t.dtype not in dtypes or t.dim() != len(shape) or any(w is not None and w != n for n, w in
+                                                            zip(t.shape, shape)):
+        raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+
+
+def _cache(kv_pool, kv_scales, page_table, q_offsets, q_vis, rows: int, B: int):
+    """Checks the latent cache and the bookkeeping of a call; returns the tokens
+    that share a scale (1 for a bf16 cache)."""
+    e4m3 = (torch.uint8, torch.float8_e4m3fn)
+    _expect("kv_pool", kv_pool, torch.bfloat16 if kv_scales is None else e4m3, None, None, DIM)
+    _expect("page_table", page_table, torch.int32, B, None)
+    _expect("q_offsets", q_offsets, torch.int32, B + 1)
+    _expect("q_vis", q_vis, torch.int32, rows)
+    if kv_scales is None:
+        return 1
+    _expect("kv_scales", kv_scales, torch.float32, kv_pool.shape[0], None)
+    n = kv_scales.shape[1]
+    if n == 0 or kv_pool.shape[1] % n:
+        raise ValueError("kv_scales: [num_pages, page_size / block]")
+    return kv_pool.shape[1] // n
+
+
+def dsa_latent_append(kv, k_pe, inv_freq, kv_pool, page_table, q_offsets, q_vis, B, ws,
+                      kv_scales=None, interleaved=False, stream=None):
+    """Appends tokens to the latent cache, the RoPE part rotated on the way: row t
+    is the token at position q_vis[t] - 1 of its sequence.  kv [T,512] and k_pe
+    [T,64] bf16 may be slices of one projection's output.  kv_scales (fp32
+    [num_pages, page_size / block]) makes it an e4m3 cache with a scale for each
+    block of tokens; see include/dsa.h."""
+    T = kv.shape[0]
+    p_kv = _rows_ptr(kv, DIM_V, torch.bfloat16, "kv")
+    p_pe = _rows_ptr(k_pe, DIM - DIM_V, torch.bfloat16, "k_pe")
+    _expect("kv", kv, torch.bfloat16, T, DIM_V)
+    _expect("k_pe", k_pe, torch.bfloat16, T, DIM - DIM_V)
+    _expect("inv_freq", inv_freq, torch.float32, (DIM - DIM_V) // 2)
+    block = _cache(kv_pool, kv_scales, page_table, q_offsets, q_vis, T, B)
+    # a single row's stride says nothing about the rows after it
+    ld_kv, ld_pe = (kv.stride(0), k_pe.stride(0)) if T > 1 else (DIM_V, DIM - DIM_V)
+    _check(lib().dsa_latent_append(
+        p_kv, ld_kv, p_pe, ld_pe, _ptr(inv_freq), int(interleaved), _ptr(page_table),
+        page_table.shape[1], _ptr(q_offsets), _ptr(q_vis), B, T, _ptr(kv_pool), _ptr(kv_scales),
+        kv_pool.shape[0], kv_pool.shape[1], block, _ptr(ws), ws.numel() * ws.element_size(),
+        _stream(stream)), "dsa_latent_append")
+
+
+def dsa_attend_workspace_bytes(heads: int) -> int:
+    return lib().dsa_attend_workspace_bytes(heads)
+
+
+def attend_workspace(heads: int = HEADS, device="cuda") -> torch.Tensor:
+    """A zeroed device workspace for dsa_mla_decode_sinks and
+    dsa_sparse_mla_decode_fp8_block (one for 128 heads also serves 64)."""
+    n = dsa_attend_workspace_bytes(heads)
+    if n == 0:
+        raise DSAError(2, "dsa_attend_workspace_bytes")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _attend_args(q, kv_pool, kv_scales, page_table, q_offsets, q_vis, B, out, lse):
+    Q, H = q.shape[0], q.shape[1]
+    _expect("q", q, torch.bfloat16, None, None, DIM)
+    _expect("out", out, torch.bfloat16, Q, H, DIM_V)
+    _expect("lse", lse, torch.float32, Q, H)
+    return Q, H, _cache(kv_pool, kv_scales, page_table, q_offsets, q_vis, Q, B)
+
+
+def dsa_mla_decode_sinks(q, kv_pool, page_table, q_offsets, q_vis, B, sinks, window, scale, out,
+                         lse, ws, kv_scales=None, stream=None):
+    """MLA decode over the first `sinks` and the last `window` visible tokens, of a
+    bf16 cache or (kv_scales) a block-scaled e4m3 one; out bf16 [Q,heads,512],
+    lse fp32 [Q,heads]; see include/dsa.h."""
+    Q, H, block = _attend_args(q, kv_pool, kv_scales, page_table, q_offsets, q_vis, B, out, lse)
+    _check(lib().dsa_mla_decode_sinks(
+        _ptr(q), _ptr(kv_pool), _ptr(kv_scales), kv_pool.shape[0], kv_pool.shape[1], block,
+        _ptr(page_table), page_table.shape[1], _ptr(q_offsets), _ptr(q_vis), B, Q, H, sinks, window,
+        float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
+        _stream(stream)), "dsa_mla_decode_sinks")
+
+
+def dsa_sparse_mla_decode_fp8_block(q, kv_pool, kv_scales, page_table, q_offsets, q_vis, idx, B,
+                                    scale, out, lse, ws, stream=None):
+    """Sparse MLA over the selected tokens of a block-scaled e4m3 cache; out bf16
+    [Q,heads,512], lse fp32 [Q,heads]; see include/dsa.h."""
+    Q, H, block = _attend_args(q, kv_pool, kv_scales, page_table, q_offsets, q_vis, B, out, lse)
+    _expect("idx", idx, torch.int32, Q, None)
+    _check(lib().dsa_sparse_mla_decode_fp8_block(
+        _ptr(q), _ptr(kv_pool), _ptr(kv_scales), kv_pool.shape[0], kv_pool.shape[1], block,
+        _ptr(page_table), page_table.shape[1], _ptr(q_offsets), _ptr(q_vis), _ptr(idx), B, Q, H,
+        idx.shape[1], float(scale), _ptr(out), _ptr(lse), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream)), "dsa_sparse_mla_decode_fp8_block")
 
 
 def dsa_lse_combine(o_parts, lse_parts, out, lse, stream=None):

@@ -523,6 +523,101 @@ dsa_status dsa_decode_step(int n_layers, int index_share, int mtp_index_share,
   return DSA_OK;
 }
 
+// the latent cache of the append and of the two attentions that read it: bf16,
+// or e4m3 with one scale for each block of tokens
+static dsa_status cache_checks(const void* kv_pool, const float* kv_scales, int num_pages,
+                               int page_size, int scale_block, const int32_t* page_table,
+                               int max_pages) {
+  if (!kv_pool || !page_table || num_pages <= 0 || max_pages <= 0) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(kv_pool)) return DSA_ERR_INVALID_ARG;
+  if (!page_size_ok(page_size, num_pages)) return DSA_ERR_UNSUPPORTED;
+  if (kv_scales) {
+    if (reinterpret_cast<uintptr_t>(kv_scales) & 3u) return DSA_ERR_INVALID_ARG;
+    if (scale_block < 1 || (scale_block & (scale_block - 1)) || scale_block > page_size)
+      return DSA_ERR_UNSUPPORTED;
+  }
+  return DSA_OK;
+}
+
+dsa_status dsa_latent_append(const void* kv, int64_t ld_kv, const void* k_pe, int64_t ld_pe,
+                             const float* inv_freq, int interleaved, const int32_t* page_table,
+                             int max_pages, const int32_t* q_offsets, const int32_t* q_vis, int B,
+                             int T, void* kv_pool, float* kv_scales, int num_pages, int page_size,
+                             int scale_block, void* ws, size_t ws_bytes, void* stream) {
+  if (!kv || !k_pe || !inv_freq || !q_offsets || !q_vis || !ws) return DSA_ERR_INVALID_ARG;
+  if (B <= 0 || T <= 0) return DSA_ERR_INVALID_ARG;
+  if (ld_kv < DSA_DIM_V || (ld_kv & 7) || !aligned16(kv)) return DSA_ERR_INVALID_ARG;
+  if (ld_pe < DSA_DIM - DSA_DIM_V || (ld_pe & 1) || (reinterpret_cast<uintptr_t>(k_pe) & 3u))
+    return DSA_ERR_INVALID_ARG;
+  dsa_status s = cache_checks(kv_pool, kv_scales, num_pages, page_size, scale_block, page_table,
+                              max_pages);
+  if (s != DSA_OK) return s;
+  if (B > DSA_MAX_BATCH) return DSA_ERR_UNSUPPORTED;
+  if (ws_bytes < 256) return DSA_ERR_WORKSPACE;
+  return cuda_status(launch_latent_append(
+      static_cast<const __nv_bfloat16*>(kv), ld_kv, static_cast<const __nv_bfloat16*>(k_pe), ld_pe,
+      inv_freq, interleaved, page_table, max_pages, q_offsets, q_vis, B, T, kv_pool, kv_scales,
+      num_pages, page_size, scale_block, static_cast<uint32_t*>(ws),
+      static_cast<cudaStream_t>(stream)));
+}
+
+size_t dsa_attend_workspace_bytes(int heads) {
+  return heads_ok(heads) ? attend_workspace_bytes(heads) : 0;
+}
+
+static dsa_status attend_checks(const void* q, const int32_t* q_offsets, const int32_t* q_vis,
+                                int B, int Q, int heads, float scale, const void* out,
+                                const float* lse, const void* ws, size_t ws_bytes) {
+  if (!q || !q_offsets || !q_vis || !out || !lse || !ws) return DSA_ERR_INVALID_ARG;
+  if (B <= 0 || Q <= 0) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return DSA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || scale > 3.0e38f) return DSA_ERR_INVALID_ARG;
+  if (!heads_ok(heads)) return DSA_ERR_UNSUPPORTED;
+  if (B > DSA_MAX_BATCH || Q > 65535) return DSA_ERR_UNSUPPORTED;
+  if (ws_bytes < attend_workspace_bytes(heads)) return DSA_ERR_WORKSPACE;
+  return DSA_OK;
+}
+
+dsa_status dsa_mla_decode_sinks(const void* q, const void* kv_pool, const float* kv_scales,
+                                int num_pages, int page_size, int scale_block,
+                                const int32_t* page_table, int max_pages, const int32_t* q_offsets,
+                                const int32_t* q_vis, int B, int Q, int heads, int sinks,
+                                int window, float scale, void* out, float* lse, void* ws,
+                                size_t ws_bytes, void* stream) {
+  dsa_status s = cache_checks(kv_pool, kv_scales, num_pages, page_size, scale_block, page_table,
+                              max_pages);
+  if (s != DSA_OK) return s;
+  if (sinks < 0 || window < 0) return DSA_ERR_INVALID_ARG;
+  if ((s = attend_checks(q, q_offsets, q_vis, B, Q, heads, scale, out, lse, ws, ws_bytes)) != DSA_OK)
+    return s;
+  return cuda_status(launch_attend(static_cast<const __nv_bfloat16*>(q), kv_pool, kv_scales, num_pages,
+                                   page_size, scale_block, page_table, max_pages, q_offsets, q_vis,
+                                   nullptr, 0, B, Q, heads, sinks, window, scale,
+                                   static_cast<__nv_bfloat16*>(out), lse, ws,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_sparse_mla_decode_fp8_block(const void* q, const void* kv_pool,
+                                           const float* kv_scales, int num_pages, int page_size,
+                                           int scale_block, const int32_t* page_table,
+                                           int max_pages, const int32_t* q_offsets,
+                                           const int32_t* q_vis, const int32_t* idx, int B, int Q,
+                                           int heads, int topk, float scale, void* out, float* lse,
+                                           void* ws, size_t ws_bytes, void* stream) {
+  if (!kv_scales || !idx || topk <= 0) return DSA_ERR_INVALID_ARG;
+  dsa_status s = cache_checks(kv_pool, kv_scales, num_pages, page_size, scale_block, page_table,
+                              max_pages);
+  if (s != DSA_OK) return s;
+  if (topk > DSA_MAX_TOPK) return DSA_ERR_UNSUPPORTED;
+  if ((s = attend_checks(q, q_offsets, q_vis, B, Q, heads, scale, out, lse, ws, ws_bytes)) != DSA_OK)
+    return s;
+  return cuda_status(launch_attend(static_cast<const __nv_bfloat16*>(q), kv_pool, kv_scales, num_pages,
+                                   page_size, scale_block, page_table, max_pages, q_offsets, q_vis,
+                                   idx, topk, B, Q, heads, 0, 0, scale,
+                                   static_cast<__nv_bfloat16*>(out), lse, ws,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
 dsa_status dsa_check_error(void* ws, void* stream) {
   if (!ws) return DSA_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

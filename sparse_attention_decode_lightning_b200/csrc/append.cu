@@ -1,0 +1,303 @@
+// Latent-cache append: the rows that the attention calls read are written here,
+// the position part rotated on the way.  Token t of sequence b sits at position p = q_vis[t] - 1 and its row is
+//   [ kv[t, 0:512] | rot(k_pe[t, 0:64]) ],
+//   rot: (x, y) -> (x cos(a) - y sin(a), y cos(a) + x sin(a)),  a = p * inv_freq[i],
+// with (x, y) = elements (i, i + 32), or (2i, 2i + 1) when interleaved.
+//
+// bf16 cache: the row rounded once.  e4m3 cache: the tokens of a block share
+// one scale s = 2^e, e the smallest with amax <= 448 * 2^e in [-40, 40]; a
+// block that already holds tokens keeps s = max(old, needed) and, when that
+// grows, its codes are rescaled by old / s (a power of two, so a code changes
+// only where it falls into e4m3's subnormals).
+//
+// The angle: p * inv_freq exceeds what fp32 resolves for far positions (1e6
+// rad has a spacing of 1/16), so it is formed in fp64 as turns, reduced to
+// [-1/2, 1/2] there, and only then rounded to fp32 for sincospi.
+//
+// Bound: bytes (1152 read, 576 or 1152 written a token).
+#include "common.cuh"
+#include "internal.h"
+
+#include <cuda_fp8.h>
+
+namespace dsa {
+namespace {
+
+constexpr int WARPS = 8;
+constexpr int THREADS = 32 * WARPS;
+constexpr int MAX_G = 64;                  // rows of the token array a CTA looks for run starts in
+constexpr int EXP_LIMIT = 40;
+
+struct AppendArgs {
+  const __nv_bfloat16* kv;
+  const __nv_bfloat16* k_pe;
+  int64_t ld_kv, ld_pe;                    // row strides in elements
+  const float* inv_freq;
+  const int32_t* page_table;
+  const int32_t* q_offsets;
+  const int32_t* q_vis;
+  uint8_t* pool;
+  float* scales;
+  uint32_t* err;
+  int max_pages, B, T, num_pages, page_shift, block_shift, G, interleaved;
+};
+
+// 16 latent values (lane's 16 consecutive dims) and one rotated pair of a row
+struct Row {
+  uint4 a, b;
+  float x, y;
+};
+
+__device__ __forceinline__ Row load_row(const AppendArgs& A, int t, int pos, float inv_freq, int lane) {
+  Row r;
+  const uint4* src = reinterpret_cast<const uint4*>(A.kv + static_cast<int64_t>(t) * A.ld_kv) + 2 * lane;
+  r.a = __ldg(src);
+  r.b = __ldg(src + 1);
+  const __nv_bfloat16* pe = A.k_pe + static_cast<int64_t>(t) * A.ld_pe;
+  const float x = __bfloat162float(pe[A.interleaved ? 2 * lane : lane]);
+  const float y = __bfloat162float(pe[A.interleaved ? 2 * lane + 1 : lane + 32]);
+  double turns = static_cast<double>(pos) * static_cast<double>(inv_freq) * 0.15915494309189535;
+  turns -= rint(turns);
+  float s, c;
+  sincospif(2.f * static_cast<float>(turns), &s, &c);
+  r.x = x * c - y * s;
+  r.y = y * c + x * s;
+  return r;
+}
+
+__device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// |v| of a finite value, 0 of any other: what counts for a block's scale
+__device__ __forceinline__ float mag(float v) {
+  const float a = fabsf(v);
+  return a <= 3.4028235e38f ? a : 0.f;
+}
+
+__device__ __forceinline__ float mag4(uint4 v) {
+  return fmaxf(fmaxf(fmaxf(mag(lo_f(v.x)), mag(hi_f(v.x))), fmaxf(mag(lo_f(v.y)), mag(hi_f(v.y)))),
+               fmaxf(fmaxf(mag(lo_f(v.z)), mag(hi_f(v.z))), fmaxf(mag(lo_f(v.w)), mag(hi_f(v.w)))));
+}
+
+__device__ __forceinline__ float row_amax(const Row& r) {
+  float m = fmaxf(fmaxf(mag4(r.a), mag4(r.b)), fmaxf(mag(r.x), mag(r.y)));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
+}
+
+// smallest e in [-40, 40] with amax <= 448 * 2^e = 1.75 * 2^(e + 8)
+__device__ __forceinline__ int needed_exp(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  if (u == 0) return -EXP_LIMIT;
+  const int k = static_cast<int>(u >> 23) - 127;          // a subnormal amax is far below the limit
+  const int e = k - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return min(EXP_LIMIT, max(-EXP_LIMIT, e));
+}
+
+// v -> e4m3 code, round to nearest even; finite values saturate at 448, the
+// others become the NaN code
+__device__ __forceinline__ uint32_t f8(float v) {
+  const float a = fabsf(v);
+  if (!(a <= 3.4028235e38f)) return 0x7Fu;
+  return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ uint32_t f8x4(uint32_t w0, uint32_t w1, float s) {
+  return f8(__fdiv_rn(lo_f(w0), s)) | (f8(__fdiv_rn(hi_f(w0), s)) << 8) |
+         (f8(__fdiv_rn(lo_f(w1), s)) << 16) | (f8(__fdiv_rn(hi_f(w1), s)) << 24);
+}
+
+__device__ __forceinline__ float f8_value(uint32_t code) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
+  return __half2float(*reinterpret_cast<const __half*>(&h));
+}
+
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float ratio) {
+  return f8(f8_value(w & 0xFFu) * ratio) | (f8(f8_value((w >> 8) & 0xFFu) * ratio) << 8) |
+         (f8(f8_value((w >> 16) & 0xFFu) * ratio) << 16) | (f8(f8_value(w >> 24) * ratio) << 24);
+}
+
+// A run: the rows of one sequence that fall into one block of the cache
+struct Run {
+  int t, n;            // first row of the token array, rows
+  int pos;             // position of the first row
+  int vis0;            // q_vis expected at row t
+  int64_t slot;        // pool row of the first row
+};
+
+// run that starts at row t, or n = 0
+__device__ __forceinline__ Run find_run(const AppendArgs& A, const int* off, int t) {
+  Run r = {t, 0, 0, 0, 0};
+  if (t < off[0] || t >= off[A.B]) return r;              // rows outside every sequence stay as they are
+  int lo = 0, hi = A.B;                                   // off[lo] <= t < off[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= t) lo = mid; else hi = mid;
+  }
+  const int f = off[lo];
+  if (f < 0 || f > t || off[lo + 1] > A.T) return r;
+  const int v0 = A.q_vis[f];
+  const int v = A.q_vis[t];
+  if (v0 <= 0) {                                          // a padded sequence
+    if (v != 0) raise_error(A.err, DEVERR_BOUNDS);
+    return r;
+  }
+  const int64_t pos = static_cast<int64_t>(v0) - 1 + (t - f);
+  const int bm = (1 << A.block_shift) - 1;
+  if (t != f && (pos & bm) != 0) return r;                // belongs to the run before
+  const int64_t page = pos >> A.page_shift;
+  const int n = min(off[lo + 1] - t, bm + 1 - static_cast<int>(pos & bm));
+  const int pg = page < A.max_pages ? A.page_table[static_cast<size_t>(lo) * A.max_pages + page] : -1;
+  if (pg < 0 || pg >= A.num_pages) {
+    // nothing to say where every row of the run is padding
+    for (int i = 0; i < n; ++i)
+      if (A.q_vis[t + i] != 0) {
+        raise_error(A.err, DEVERR_BOUNDS);
+        break;
+      }
+    return r;
+  }
+  r.n = n;
+  r.pos = static_cast<int>(pos);
+  r.vis0 = r.pos + 1;
+  r.slot = (static_cast<int64_t>(pg) << A.page_shift) + (pos & ((1 << A.page_shift) - 1));
+  return r;
+}
+
+// W warps a run: 1 where runs are short (decode, small blocks), 8 where they
+// are long.  One row a warp at a time.
+template <bool KV8, int W>
+__global__ void __launch_bounds__(THREADS) latent_append_kernel(const __grid_constant__ AppendArgs A) {
+  __shared__ int off[DSA_MAX_BATCH + 1];
+  __shared__ Run runs[MAX_G];
+  __shared__ int n_runs;
+  __shared__ float wmax[WARPS];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) n_runs = 0;
+  for (int i = tid; i <= A.B; i += THREADS) off[i] = A.q_offsets[i];
+  __syncthreads();
+  if (tid < A.G) {
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * A.G + tid;
+    if (t < A.T) {
+      const Run r = find_run(A, off, static_cast<int>(t));
+      if (r.n > 0) runs[atomicAdd(&n_runs, 1)] = r;       // any order: runs are independent
+    }
+  }
+  __syncthreads();
+  const float inv_freq = A.inv_freq[lane];
+  constexpr int GROUPS = WARPS / W;
+  const int group = warp / W, wg = warp % W;
+  for (int k = group; k < n_runs; k += GROUPS) {
+    const Run r = runs[k];
+    if constexpr (!KV8) {
+      for (int i = wg; i < r.n; i += W) {
+        const int v = A.q_vis[r.t + i];
+        if (v != r.vis0 + i) {
+          if (v != 0 && lane == 0) raise_error(A.err, DEVERR_BOUNDS);
+          continue;
+        }
+        const Row w = load_row(A, r.t + i, r.pos + i, inv_freq, lane);
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(A.pool) + (r.slot + i) * DSA_DIM;
+        reinterpret_cast<uint4*>(dst)[2 * lane] = w.a;
+        reinterpret_cast<uint4*>(dst)[2 * lane + 1] = w.b;
+        dst[DSA_DIM_V + (A.interleaved ? 2 * lane : lane)] = __float2bfloat16_rn(w.x);
+        dst[DSA_DIM_V + (A.interleaved ? 2 * lane + 1 : lane + 32)] = __float2bfloat16_rn(w.y);
+      }
+    } else {
+      const int held = r.pos & ((1 << A.block_shift) - 1);   // tokens the block holds already
+      float* sp = A.scales + (r.slot >> A.block_shift);
+      const float old = held ? *sp : 0.f;
+      float m = 0.f;
+      bool any = false;
+      for (int i = wg; i < r.n; i += W) {
+        const int v = A.q_vis[r.t + i];
+        if (v != r.vis0 + i) {
+          if (v != 0 && lane == 0) raise_error(A.err, DEVERR_BOUNDS);
+          continue;
+        }
+        any = true;
+        m = fmaxf(m, row_amax(load_row(A, r.t + i, r.pos + i, inv_freq, lane)));
+      }
+      if constexpr (W > 1) {
+        if (lane == 0) wmax[warp] = any ? m : -1.f;
+        __syncthreads();
+        m = -1.f;
+#pragma unroll
+        for (int i = 0; i < WARPS; ++i) m = fmaxf(m, wmax[i]);
+        any = m >= 0.f;
+        __syncthreads();                                   // wmax is free, every thread holds `old`
+      }
+      if (!any) continue;                                  // nothing but padding
+      float s = exp2f(static_cast<float>(needed_exp(m)));
+      const bool old_ok = old >= 0x1p-40f && old <= 0x1p40f;
+      if (held && !old_ok && lane == 0 && wg == 0) raise_error(A.err, DEVERR_BOUNDS);
+      if (held && old_ok) s = fmaxf(s, old);
+      __syncwarp();
+      if (lane == 0 && wg == 0) *sp = s;
+      if (held && old_ok && s > old) {
+        const float ratio = __fdiv_rn(old, s);
+        uint4* base = reinterpret_cast<uint4*>(A.pool + (r.slot - held) * DSA_DIM);
+        for (int i = wg * 32 + lane; i < held * (DSA_DIM / 16); i += 32 * W) {
+          uint4 c = base[i];
+          c = make_uint4(rescale4(c.x, ratio), rescale4(c.y, ratio), rescale4(c.z, ratio), rescale4(c.w, ratio));
+          base[i] = c;
+        }
+      }
+      for (int i = wg; i < r.n; i += W) {
+        if (A.q_vis[r.t + i] != r.vis0 + i) continue;
+        const Row w = load_row(A, r.t + i, r.pos + i, inv_freq, lane);
+        uint8_t* dst = A.pool + (r.slot + i) * DSA_DIM;
+        reinterpret_cast<uint4*>(dst)[lane] = make_uint4(f8x4(w.a.x, w.a.y, s), f8x4(w.a.z, w.a.w, s),
+                                                         f8x4(w.b.x, w.b.y, s), f8x4(w.b.z, w.b.w, s));
+        dst[DSA_DIM_V + (A.interleaved ? 2 * lane : lane)] = static_cast<uint8_t>(f8(__fdiv_rn(w.x, s)));
+        dst[DSA_DIM_V + (A.interleaved ? 2 * lane + 1 : lane + 32)] = static_cast<uint8_t>(f8(__fdiv_rn(w.y, s)));
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_latent_append(const __nv_bfloat16* kv, int64_t ld_kv, const __nv_bfloat16* k_pe,
+                                 int64_t ld_pe, const float* inv_freq, int interleaved,
+                                 const int32_t* page_table, int max_pages, const int32_t* q_offsets,
+                                 const int32_t* q_vis, int B, int T, void* pool, float* scales,
+                                 int num_pages, int page_size, int scale_block, uint32_t* err,
+                                 cudaStream_t st) {
+  AppendArgs A = {};
+  A.kv = kv;
+  A.k_pe = k_pe;
+  A.ld_kv = ld_kv;
+  A.ld_pe = ld_pe;
+  A.inv_freq = inv_freq;
+  A.page_table = page_table;
+  A.q_offsets = q_offsets;
+  A.q_vis = q_vis;
+  A.pool = static_cast<uint8_t*>(pool);
+  A.scales = scales;
+  A.err = err;
+  A.max_pages = max_pages;
+  A.B = B;
+  A.T = T;
+  A.num_pages = num_pages;
+  while ((1 << A.page_shift) < page_size) ++A.page_shift;
+  while (scales && (1 << A.block_shift) < scale_block) ++A.block_shift;   // bf16: runs of one row
+  A.interleaved = interleaved;
+  // rows a CTA looks for run starts in: enough CTAs to fill the GPU four deep
+  const int fill = 4 * device_sm_count();
+  A.G = T / fill < 1 ? 1 : (T / fill > MAX_G ? MAX_G : T / fill);
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) + A.G - 1) / A.G);
+  if (!scales) {
+    latent_append_kernel<false, 1><<<grid, THREADS, 0, st>>>(A);
+  } else {
+    // rows a run can have: a warp takes short runs alone
+    const int per_seq = (T + B - 1) / B;
+    const int rows = per_seq < scale_block ? per_seq : scale_block;
+    if (rows <= 4) latent_append_kernel<true, 1><<<grid, THREADS, 0, st>>>(A);
+    else latent_append_kernel<true, 8><<<grid, THREADS, 0, st>>>(A);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

@@ -132,6 +132,23 @@ cudaError_t launch_combine_layers(const float* o_part, const float* l_part, int 
 cudaError_t launch_combine(const float* o_part, const float* l_part, int Q, int S, int H,
                            float* out, float* lse, cudaStream_t st, bool pdl);
 
+// the latent-cache append (append.cu); scales null: a bf16 cache
+cudaError_t launch_latent_append(const __nv_bfloat16* kv, int64_t ld_kv, const __nv_bfloat16* k_pe,
+                                 int64_t ld_pe, const float* inv_freq, int interleaved,
+                                 const int32_t* page_table, int max_pages, const int32_t* q_offsets,
+                                 const int32_t* q_vis, int B, int T, void* pool, float* scales,
+                                 int num_pages, int page_size, int scale_block, uint32_t* err,
+                                 cudaStream_t st);
+
+// attention over a token list (attend_sm100.cu): selected positions when idx
+// is given (e4m3 cache only), else sinks and window; kv_scales null: a bf16 cache
+size_t attend_workspace_bytes(int H);
+cudaError_t launch_attend(const __nv_bfloat16* q, const void* pool, const float* kv_scales,
+                          int num_pages, int page_size, int scale_block, const int32_t* page_table,
+                          int max_pages, const int32_t* q_offsets, const int32_t* q_vis,
+                          const int32_t* idx, int topk, int B, int Q, int H, int sinks, int window,
+                          float scale, __nv_bfloat16* out, float* lse, void* ws, cudaStream_t st);
+
 // pdl = true: the kernel may start before the previous kernel on the stream
 // ends (programmatic dependent launch); it waits for it in pdl_wait().  Only
 // set where the previous kernel is one of this library's, launched by the same
