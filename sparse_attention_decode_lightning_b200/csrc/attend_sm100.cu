@@ -32,9 +32,9 @@
 // Tensor memory (512 columns): O [0,256) | scores slot 0 [256,320) | slot 1
 // [320,384) | the 256 query dims that are also this CTA's value dims [384,512).
 // P overwrites its slot's scores.  Shared memory: the other 320 query dims
-// (80 KB), two stages of value chunks (4 x 8 KB each), a ring of 9 chunks for
-// the 5 other chunks of a tile.  A chunk is 64 tokens x 64 dims, 16 bits, in
-// the 128-byte swizzle.
+// (80 KB), three stages of value chunks (4 x 8 KB each), one stage of the 5
+// other chunks of a tile, refilled by halves while the tile's values run.  A
+// chunk is 64 tokens x 64 dims, 16 bits, in the 128-byte swizzle.
 //
 // Roles (512 threads): warp 0 issues the MMAs; warps 1..3 look up the pool
 // rows (list -> page table -> scale) up to six tiles ahead, since each is a
@@ -54,32 +54,33 @@ namespace {
 constexpr int NR = 64;                               // tokens per tile
 constexpr int CH = NR * 128;                         // chunk bytes: 64 tokens x 64 dims x 2
 constexpr int QCH = 128 * 128;                       // query chunk bytes: 128 heads x 64 dims x 2
-constexpr int XC = 5;                                // chunks of a tile that are scores only
-constexpr int VC = 4;                                // chunks that are values too
-constexpr int XRING = 9;
-constexpr int NVS = 2;                               // value stages
+constexpr int AC = 4;                                // latent chunks of a tile that are scores only
+constexpr int VC = 4;                                // chunks that are values too (one more: positions)
+constexpr int NV = 3;                                // value stages
 constexpr int RR = 6;                                // tiles looked up ahead
 constexpr int RESOLVERS = 3;
 constexpr int SMX = 4;                               // softmax warps
-constexpr int LOADERS = 8;
+constexpr int GROUP = 4;                             // warps of each of the two loader groups
+constexpr int LOADERS = 2 * GROUP;
 constexpr int THREADS = 32 * (1 + RESOLVERS + SMX + LOADERS);
-constexpr int LT = 32 * LOADERS;
 
 constexpr int OFF_QX = 0;
-constexpr int OFF_V = OFF_QX + XC * QCH;
-constexpr int OFF_X = OFF_V + NVS * VC * CH;
-constexpr int OFF_ROWS = OFF_X + XRING * CH;         // int32 [RR][64]: pool row or -1
-constexpr int OFF_COL = OFF_ROWS + RR * NR * 4;      // float4 [RR][64]: scale, log2 s, 1 / s
-constexpr int OFF_MASK = OFF_COL + RR * NR * 16;     // uint32 [RR][2]: tokens that count
+constexpr int OFF_V = OFF_QX + (AC + 1) * QCH;       // [3][4] value chunks
+constexpr int OFF_A = OFF_V + NV * VC * CH;          // [5] chunks of the other half, and the positions
+constexpr int OFF_COL = OFF_A + (AC + 1) * CH;       // float4 [RR][64]: scale, log2 s, 1 / s of each token
+constexpr int OFF_TILE = OFF_COL + RR * NR * 16;     // float4 [RR]: the same for a whole tile; w: it holds
+constexpr int OFF_ROWS = OFF_TILE + RR * 16;         // int32 [RR][64]: pool row or -1
+constexpr int OFF_FOLD = OFF_ROWS + RR * NR * 4;     // uint16 [RR][64]: fp16 factor of a token's codes
+constexpr int OFF_MASK = OFF_FOLD + RR * NR * 2;     // uint32 [RR][2]: tokens that count
 constexpr int OFF_QMUL = OFF_MASK + RR * 2 * 4;      // float [128]
 constexpr int OFF_SCAN = OFF_QMUL + 128 * 4;         // int64 [17], then the first query and its tile
 constexpr int OFF_BAR = OFF_SCAN + 20 * 8;
-constexpr int NBAR = 2 * RR + 2 * XRING + 2 * NVS + 2 + 2 + 2 + 3;
+constexpr int NBAR = 2 * RR + 4 * 2 + 2 * NV + 3;
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
 static_assert(SMEM_BYTES <= 232448, "shared memory exceeds the sm_100 limit");
-static_assert(4 * QCH == NVS * VC * CH, "the query's value-dim chunks pass through the value stages");
-static_assert(OFF_V % 1024 == 0 && OFF_X % 1024 == 0, "swizzle atoms");
+static_assert(4 * QCH <= NV * VC * CH, "the query's value-dim chunks pass through the value stages");
+static_assert(OFF_V % 1024 == 0 && OFF_A % 1024 == 0, "swizzle atoms");
 constexpr uint32_t O_COL = 0, S_COL = 256, Q_COL = 384, TMEM_COLS = 512;
 
 struct AttendArgs {
@@ -155,12 +156,22 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// four e4m3 codes -> four fp16, exactly
-__device__ __forceinline__ uint2 widen4(uint32_t w) {
-  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3);
-  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
-  return make_uint2(static_cast<uint32_t>(a.x) | (static_cast<uint32_t>(a.y) << 16),
-                    static_cast<uint32_t>(b.x) | (static_cast<uint32_t>(b.y) << 16));
+// four e4m3 codes -> four fp16 times f (a power of two), exactly
+__device__ __forceinline__ uint2 widen4(uint32_t w, __half2 f) {
+  const __half2 a = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3)), f);
+  const __half2 b = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3)), f);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 
 // larger magnitude bits of a bf16 pair's two values, seen as two u16
@@ -177,23 +188,24 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* qx = smem + OFF_QX;
   uint8_t* vst = smem + OFF_V;
-  uint8_t* xst = smem + OFF_X;
+  uint8_t* ast = smem + OFF_A;
   int* rows = reinterpret_cast<int*>(smem + OFF_ROWS);
   float4* col = reinterpret_cast<float4*>(smem + OFF_COL);
+  float4* tsc = reinterpret_cast<float4*>(smem + OFF_TILE);
+  uint16_t* fold = reinterpret_cast<uint16_t*>(smem + OFF_FOLD);
   uint32_t* mask = reinterpret_cast<uint32_t*>(smem + OFF_MASK);
   float* qmul = reinterpret_cast<float*>(smem + OFF_QMUL);
   int64_t* scan = reinterpret_cast<int64_t*>(smem + OFF_SCAN);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint64_t* r_full = bars;                 // [RR] rows of a tile are looked up
   uint64_t* r_empty = r_full + RR;
-  uint64_t* x_full = r_empty + RR;         // [XRING]
-  uint64_t* x_empty = x_full + XRING;
-  uint64_t* v_full = x_empty + XRING;      // [NVS]
-  uint64_t* v_empty = v_full + NVS;
-  uint64_t* s_full = v_empty + NVS;        // [2] scores of a tile are in their slot
+  uint64_t* a_full = r_empty + RR;         // [2] chunks 0, 1 of a tile, then 2, 3 and the positions
+  uint64_t* a_empty = a_full + 2;          // [2] the scores have read them
+  uint64_t* s_full = a_empty + 2;          // [2] scores of a tile are in their slot
   uint64_t* p_full = s_full + 2;           // [2] P of a tile is in its slot
-  uint64_t* s_free = p_full + 2;           // [2] the value MMA of the slot's tile is done
-  uint64_t* q_staged = s_free + 2;         // a segment's query is in shared memory
+  uint64_t* v_full = p_full + 2;           // [NV] a tile's value chunks
+  uint64_t* v_free = v_full + NV;          // [NV] the value MMA is done: its stage and scores slot are free
+  uint64_t* q_staged = v_free + NV;        // a segment's query is in shared memory
   uint64_t* q_ready = q_staged + 1;        // ... and its value dims in tensor memory
   uint64_t* o_final = q_ready + 1;         // every MMA of a segment is done
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
@@ -207,18 +219,15 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       mbar_init(&r_full[i], 1);
       mbar_init(&r_empty[i], LOADERS + SMX);
     }
-    for (int i = 0; i < XRING; ++i) {
-      mbar_init(&x_full[i], KV8 ? LOADERS : LT);
-      mbar_init(&x_empty[i], 1);
-    }
-    for (int i = 0; i < NVS; ++i) {
-      mbar_init(&v_full[i], KV8 ? LOADERS : LT);
-      mbar_init(&v_empty[i], 1);
-    }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&a_full[i], GROUP);
+      mbar_init(&a_empty[i], 1);
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], SMX);
-      mbar_init(&s_free[i], 1);
+    }
+    for (int i = 0; i < NV; ++i) {
+      mbar_init(&v_full[i], GROUP);
+      mbar_init(&v_free[i], 1);
     }
     mbar_init(q_staged, LOADERS);
     mbar_init(q_ready, SMX);
@@ -268,63 +277,88 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
 
   if (warp == 0) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t fmt = KV8 ? 0u /*F16*/ : 1u /*BF16*/;
-      constexpr uint32_t idesc_s = umma_idesc(fmt, 128, NR);
-      constexpr uint32_t idesc_pv = umma_idesc(fmt, 128, 256, 0, 1);
-      const uint32_t qa_s = smem_u32(qx);
-      bool ok = true;
-      int q = q0, off = off0, left = ntile;
-      uint32_t g = 0;                              // tiles so far
-      for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
-        const int n = min(tiles_of<IDX>(a, q) - off, left);
-        left -= n;
-        if (!(ok = mbar_wait(q_ready, seg & 1, a.err))) break;
-        tc_fence_after();
-        for (int u = 0; u <= n && ok; ++u) {
-          if (u < n) {
-            const uint32_t gu = g + u, sb = gu & 1, vs = gu % NVS;
-            const uint32_t d = tmem + S_COL + sb * NR;
-            if (!(ok = mbar_wait(&s_free[sb], ((gu >> 1) & 1) ^ 1, a.err))) break;
-            for (int c = 0; c < XC; ++c) {
-              const uint32_t x = gu * XC + c, slot = x % XRING;
-              if (!(ok = mbar_wait(&x_full[slot], (x / XRING) & 1, a.err))) break;
-              fence_proxy_async_smem();
-              tc_fence_after();
-              const uint32_t ka = smem_u32(xst + slot * CH);
+    // The warp walks together, so that descriptors stay in uniform registers,
+    // and one elected lane issues.  The loaders fence their own writes.
+    constexpr uint32_t fmt = KV8 ? 0u /*F16*/ : 1u /*BF16*/;
+    constexpr uint32_t idesc_s = umma_idesc(fmt, 128, NR);
+    constexpr uint32_t idesc_pv = umma_idesc(fmt, 128, 256, 0, 1);
+    const uint64_t dq = umma_desc_sw128(smem_u32(qx), 1024, 16);
+    const uint64_t da = umma_desc_sw128(smem_u32(ast), 1024, 16);
+    const uint64_t dv = umma_desc_sw128(smem_u32(vst), 1024, 16);
+    const uint64_t dm = umma_desc_sw128_mn(smem_u32(vst), CH, 1024);
+    const bool lead = elect_one();
+    bool ok = true;
+    int q = q0, off = off0, left = ntile;
+    uint32_t g = 0;                              // tiles so far
+    for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
+      const int n = min(tiles_of<IDX>(a, q) - off, left);
+      left -= n;
+      if (!(ok = wwait(q_ready, seg & 1, a.err))) break;
+      tc_fence_after();
+      // values of tile u - 1 between the scores of tile u, so that neither the
+      // softmax before nor the free slot after is waited for
+      for (int u = 0; u <= n && ok; ++u) {
+        const uint32_t gu = g + u, sb = gu & 1, vs = gu % NV;
+        const uint32_t d = tmem + S_COL + sb * NR;
+        if (u < n) {
+          // P of tile u - 2 has left the slot
+          if (gu >= 2 && !(ok = wwait(&v_free[(gu - 2) % NV], ((gu - 2) / NV) & 1, a.err))) break;
+          if (!(ok = wwait(&a_full[0], gu & 1, a.err))) break;
+          tc_fence_after();
+          if (lead) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_f16(d, umma_desc_sw128(qa_s + c * QCH + k * 32, 1024, 16),
-                        umma_desc_sw128(ka + k * 32, 1024, 16), idesc_s, c > 0 || k > 0);
-              mma_commit(&x_empty[slot]);
-            }
-            if (!ok) break;
-            if (!(ok = mbar_wait(&v_full[vs], (gu / NVS) & 1, a.err))) break;
-            fence_proxy_async_smem();
-            tc_fence_after();
-            const uint32_t va = smem_u32(vst + vs * VC * CH);
+            for (int k = 0; k < 8; ++k)
+              mma_f16(d, dq + (k >> 2) * (QCH >> 4) + (k & 3) * 2, da + (k >> 2) * (CH >> 4) + (k & 3) * 2, idesc_s,
+                      k > 0);
+            mma_commit(&a_empty[0]);
+          }
+          __syncwarp();
+          if (!(ok = wwait(&a_full[1], gu & 1, a.err))) break;
+          tc_fence_after();
+          if (lead) {
 #pragma unroll
-            for (int k = 0; k < 4 * VC; ++k)
-              mma_f16_ts(d, tmem + Q_COL + k * 8, umma_desc_sw128(va + (k >> 2) * CH + (k & 3) * 32, 1024, 16),
+            for (int k = 8; k < 4 * (AC + 1); ++k)
+              mma_f16(d, dq + (k >> 2) * (QCH >> 4) + (k & 3) * 2, da + (k >> 2) * (CH >> 4) + (k & 3) * 2, idesc_s,
+                      1u);
+            mma_commit(&a_empty[1]);
+          }
+          __syncwarp();
+          if (!(ok = wwait(&v_full[vs], (gu / NV) & 1, a.err))) break;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              mma_f16_ts(d, tmem + Q_COL + k * 8, dv + vs * (VC * CH >> 4) + (k >> 2) * (CH >> 4) + (k & 3) * 2,
+                         idesc_s, 1u);
+          }
+          __syncwarp();
+        }
+        if (u >= 1) {
+          const uint32_t gt = gu - 1, tb = gt & 1, ts = gt % NV;
+          if (!(ok = wwait(&p_full[tb], (gt >> 1) & 1, a.err))) break;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int k = 0; k < NR / 16; ++k)
+              mma_f16_ts(tmem + O_COL, tmem + S_COL + tb * NR + k * 8, dm + ts * (VC * CH >> 4) + k * (2048 >> 4),
+                         idesc_pv, (u > 1 || k > 0) ? 1u : 0u);
+            mma_commit(&v_free[ts]);
+            if (u == n) mma_commit(o_final);
+          }
+          __syncwarp();
+        }
+        if (u < n) {
+          if (lead) {
+#pragma unroll
+            for (int k = 8; k < 4 * VC; ++k)
+              mma_f16_ts(d, tmem + Q_COL + k * 8, dv + vs * (VC * CH >> 4) + (k >> 2) * (CH >> 4) + (k & 3) * 2,
                          idesc_s, 1u);
             mma_commit(&s_full[sb]);
           }
-          if (u >= 1) {
-            const uint32_t gt = g + u - 1, sb = gt & 1, vs = gt % NVS;
-            if (!(ok = mbar_wait(&p_full[sb], (gt >> 1) & 1, a.err))) break;
-            tc_fence_after();
-            const uint32_t va = smem_u32(vst + vs * VC * CH);
-#pragma unroll
-            for (int k = 0; k < NR / 16; ++k)
-              mma_f16_ts(tmem + O_COL, tmem + S_COL + sb * NR + k * 8,
-                         umma_desc_sw128_mn(va + k * 2048, CH, 1024), idesc_pv, (u > 1 || k > 0) ? 1u : 0u);
-            mma_commit(&v_empty[vs]);
-            mma_commit(&s_free[sb]);
-            if (u == n) mma_commit(o_final);
-          }
+          __syncwarp();
         }
-        g += n;
       }
+      g += n;
     }
   } else if (warp < 1 + RESOLVERS) {
     // ------------------------------------------------------------ row look-up
@@ -368,13 +402,43 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         }
         ok = wwait(&r_empty[slot], ((g / RR) & 1) ^ 1, a.err);
         if (!ok) break;
+        if constexpr (KV8) {
+          // Scales that differ by powers of two, up to 2^15, go into the fp16
+          // codes, exactly (a code is a multiple of 2^-9, fp16's least step is
+          // 2^-24): the tile then has one scale, its largest.  Other tiles keep
+          // one a token.
+          uint32_t lo = 0xffffffffu, hi = 0, mlo = 0xffffffffu, mhi = 0;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t bits = __float_as_uint(s[i]);
+            if (row[i] >= 0) {
+              lo = min(lo, bits);
+              hi = max(hi, bits);
+              mlo = min(mlo, bits & 0x7FFFFFu);
+              mhi = max(mhi, bits & 0x7FFFFFu);
+            }
+          }
+          lo = __reduce_min_sync(0xffffffffu, lo);
+          hi = __reduce_max_sync(0xffffffffu, hi);
+          mlo = __reduce_min_sync(0xffffffffu, mlo);
+          mhi = __reduce_max_sync(0xffffffffu, mhi);
+          const bool one = hi == 0 || (mlo == mhi && (hi - lo) >> 23 <= 15);
+          const float st = hi == 0 ? 1.f : __uint_as_float(hi);
+          if (lane == 0)
+            tsc[slot] = make_float4(st * a.scale_log2, log2f(st), __fdiv_rn(1.f, st), one ? 1.f : 0.f);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t down = one && row[i] >= 0 ? (hi - __float_as_uint(s[i])) >> 23 : 0u;
+            fold[slot * NR + 32 * i + lane] = down < 15 ? static_cast<uint16_t>((15 - down) << 10) : uint16_t{0x200};
+            if (!one)
+              col[slot * NR + 32 * i + lane] =
+                  row[i] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
+                             : make_float4(s[i] * a.scale_log2, log2f(s[i]), __fdiv_rn(1.f, s[i]), 0.f);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           rows[slot * NR + 32 * i + lane] = row[i];
-          if constexpr (KV8)
-            col[slot * NR + 32 * i + lane] =
-                row[i] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
-                           : make_float4(s[i] * a.scale_log2, log2f(s[i]), __fdiv_rn(1.f, s[i]), 0.f);
           const uint32_t m = __ballot_sync(0xffffffffu, row[i] >= 0);
           if (lane == 0) mask[slot * 2 + i] = m;
         }
@@ -429,15 +493,18 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         tmem_ld_wait();
         const uint32_t m0 = mask[slot * 2], m1 = mask[slot * 2 + 1];
         const float4* cp = col + slot * NR;
-        if constexpr (KV8) {
+        float4 ts = make_float4(a.scale_log2, 0.f, 1.f, 1.f);
+        if constexpr (KV8) ts = tsc[slot];
+        if (!KV8 || ts.w != 0.f) {
+          const float k = ts.x * qm;
+#pragma unroll
+          for (int j = 0; j < NR; ++j) z[j] = fmaf(z[j], k, ts.y);
+        } else {
 #pragma unroll
           for (int j = 0; j < NR; ++j) {
             const float2 k = *reinterpret_cast<const float2*>(cp + j);
             z[j] = fmaf(z[j] * qm, k.x, k.y);
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < NR; ++j) z[j] *= a.scale_log2;
         }
         if ((m0 & m1) != 0xffffffffu) {
 #pragma unroll
@@ -464,17 +531,29 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
         const float m_eff = m_use == -INFINITY ? 0.f : m_use;
         float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < NR; ++j) {
-          z[j] = fast_exp2(z[j] - m_eff);
-          if constexpr (KV8) ps[j & 3] = fmaf(z[j], cp[j].z, ps[j & 3]);
-          else ps[j & 3] += z[j];
+        for (int hh = 0; hh < 2; ++hh) {
+          float* zh = z + 32 * hh;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) zh[j] = fast_exp2(zh[j] - m_eff);
+          if (!KV8 || ts.w != 0.f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) ps[j & 3] += zh[j];
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) ps[j & 3] = fmaf(zh[j], cp[32 * hh + j].z, ps[j & 3]);
+          }
+          float pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            pk[j] = __uint_as_float(KV8 ? f16x2_bits(zh[2 * j], zh[2 * j + 1]) : bf16x2_bits(zh[2 * j], zh[2 * j + 1]));
+          tmem_st16(lane_base + S_COL + sb * NR + 16 * hh, pk);
         }
-        l = l * alpha + ((ps[0] + ps[1]) + (ps[2] + ps[3]));
+        l = fmaf(l, alpha, ((ps[0] + ps[1]) + (ps[2] + ps[3])) * (KV8 && ts.w != 0.f ? ts.z : 1.f));
         __syncwarp();
         if (lane == 0) mbar_arrive(&r_empty[slot]);
         if (__any_sync(0xffffffffu, resc)) {
           // after the value MMA of the tile before
-          if (ok) ok = wwait(&s_free[(g - 1) & 1], ((g - 1) >> 1) & 1, a.err);
+          if (ok) ok = wwait(&v_free[(g - 1) % NV], ((g - 1) / NV) & 1, a.err);
           tc_fence_after();
           for (int c = 0; c < 8; ++c) {
             float o[32];
@@ -485,11 +564,6 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             tmem_st32(lane_base + O_COL + c * 32, o);
           }
         }
-        float pk[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-          pk[j] = __uint_as_float(KV8 ? f16x2_bits(z[2 * j], z[2 * j + 1]) : bf16x2_bits(z[2 * j], z[2 * j + 1]));
-        tmem_st32(lane_base + S_COL + sb * NR, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -535,8 +609,12 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
     }
   } else {
     // ------------------------------------------------------------ loaders
+    // Two groups of four warps, so that neither waits for the other's stage:
+    // group 0 fills the scores-only chunks (one stage, handed over in halves),
+    // group 1 the value chunks (three stages).
     const int lw = warp - (1 + RESOLVERS + SMX);
-    const int lt = lw * 32 + lane;
+    const bool vals = lw >= GROUP;
+    const int lt = (lw & (GROUP - 1)) * 32 + lane;
     bool ok = true;
     int q = q0, off = off0, left = ntile;
     uint32_t g = 0;
@@ -579,7 +657,7 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
             if (k == 2 && lane >= 8) continue;
             const int p = 32 * k + lane, c = p >> 3;
             const int sw = h * 128 + (((p & 7) ^ (h & 7)) << 4);
-            const int x = c == 8 ? 4 : (c & 3);
+            const int x = c == 8 ? AC : (c & 3);
             uint8_t* dst = c < 8 && (c >> 2) == half ? vst + (c & 3) * QCH : qx + x * QCH;
             *reinterpret_cast<uint4*>(dst + sw) = v[i][k];
           }
@@ -589,95 +667,127 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
       __syncwarp();
       if (lane == 0) mbar_arrive(q_staged);
 
-      // the tiles: chunk order is the 4 of the other half, the position chunk, the 4 value chunks
+      auto wait_a = [&](uint32_t gg, int part) { return wwait(&a_empty[part], (gg & 1) ^ 1, a.err); };
+      auto wait_v = [&](uint32_t gg, bool first) {
+        if (first && !wwait(q_ready, seg & 1, a.err)) return false;   // the query has left the stages
+        return wwait(&v_free[gg % NV], ((gg / NV) & 1) ^ 1, a.err);
+      };
+      auto done = [&](uint64_t* bar) {                               // the writes are for the tensor core
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+      };
       if constexpr (KV8) {
-        // thread: token lt / 4, 16 codes of each chunk; a tile's pieces are
-        // all in flight before the tile before is widened and stored
-        const int r = lt >> 2, u4 = lt & 3;
-        uint4 va[9], vb[9];
-        auto fetch = [&](uint4* v, uint32_t gg) {
+        // thread: 16 + 16 codes of each chunk of one token; a tile's pieces are
+        // all in flight before the tile before is widened and stored.  The
+        // rows of a quarter warp, r & 7 in {0,1,4,5} or {2,3,6,7}, put its 16-byte
+        // stores into eight different bank groups.
+        const int rj = lt >> 1, u2 = lt & 1;
+        const int r = (rj & ~7) | (rj & 1) | ((rj & 2) << 1) | ((rj & 4) >> 1);
+        uint4 va[2 * (AC + 1)], vb[2 * (AC + 1)];
+        __half2 fa, fb;
+        auto fetch = [&](uint4* v, __half2& f, uint32_t gg) {
           const uint32_t slot = gg % RR;
           ok = ok && wwait(&r_full[slot], (gg / RR) & 1, a.err);
           const int row = ok ? rows[slot * NR + r] : -1;
-          const uint4* src = reinterpret_cast<const uint4*>(a.pool + static_cast<size_t>(row < 0 ? 0 : row) * DSA_DIM) + u4;
+          f = __half2half2(__ushort_as_half(fold[slot * NR + r]));
+          const uint4* src = reinterpret_cast<const uint4*>(a.pool + static_cast<size_t>(row < 0 ? 0 : row) * DSA_DIM) + u2;
+          const int c0 = 4 * (vals ? half : half ^ 1);
 #pragma unroll
-          for (int c = 0; c < 9; ++c) {
-            const int dc = c < 4 ? 4 * (half ^ 1) + c : c == 4 ? 8 : 4 * half + (c - 5);
-            v[c] = row >= 0 ? __ldg(src + 4 * dc) : make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < AC + 1; ++c) {
+            const int dc = c < 4 ? c0 + c : 8;
+            const bool get = row >= 0 && (c < 4 || !vals);
+            v[2 * c] = get ? __ldg(src + 4 * dc) : make_uint4(0u, 0u, 0u, 0u);
+            v[2 * c + 1] = get ? __ldg(src + 4 * dc + 2) : make_uint4(0u, 0u, 0u, 0u);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&r_empty[slot]);
         };
-        auto store = [&](const uint4* v, uint32_t gg, bool first) {
-          const int s0 = r * 128 + (((2 * u4) ^ (r & 7)) << 4), s1 = r * 128 + (((2 * u4 + 1) ^ (r & 7)) << 4);
-          const uint32_t vs = gg % NVS;
+        // pieces 2 u2 + {0, 1} and 4 + 2 u2 + {0, 1} of token r's 128 bytes
+        auto put = [&](uint8_t* dst, const uint4* v, __half2 f) {
 #pragma unroll
-          for (int c = 0; c < 9; ++c) {
-            uint8_t* dst;
-            if (c < XC) {
-              const uint32_t x = gg * XC + c, slot = x % XRING;
-              ok = ok && wwait(&x_empty[slot], ((x / XRING) & 1) ^ 1, a.err);
-              dst = xst + slot * CH;
-            } else {
-              if (c == XC) {
-                ok = ok && wwait(&v_empty[vs], ((gg / NVS) & 1) ^ 1, a.err);
-                if (first) ok = ok && wwait(q_ready, seg & 1, a.err);   // the query has left the stages
-              }
-              dst = vst + vs * VC * CH + (c - XC) * CH;
-            }
-            if (!ok) return;
-            const uint2 a0 = widen4(v[c].x), a1 = widen4(v[c].y), a2 = widen4(v[c].z), a3 = widen4(v[c].w);
-            *reinterpret_cast<uint4*>(dst + s0) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-            *reinterpret_cast<uint4*>(dst + s1) = make_uint4(a2.x, a2.y, a3.x, a3.y);
-            if (c < XC || c == 8) {
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(c < XC ? &x_full[(gg * XC + c) % XRING] : &v_full[vs]);
-            }
+          for (int i = 0; i < 2; ++i) {
+            const uint2 a0 = widen4(v[i].x, f), a1 = widen4(v[i].y, f), a2 = widen4(v[i].z, f), a3 = widen4(v[i].w, f);
+            const int p = 4 * i + 2 * u2;
+            *reinterpret_cast<uint4*>(dst + r * 128 + ((p ^ (r & 7)) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((p + 1) ^ (r & 7)) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
           }
         };
-        fetch(va, g);
+        auto store = [&](const uint4* v, __half2 f, uint32_t gg, bool first) {
+          if (vals) {
+            if (!(ok = wait_v(gg, first))) return;
+#pragma unroll
+            for (int c = 0; c < VC; ++c) put(vst + (gg % NV) * (VC * CH) + c * CH, v + 2 * c, f);
+            done(&v_full[gg % NV]);
+          } else {
+            if (!(ok = wait_a(gg, 0))) return;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) put(ast + c * CH, v + 2 * c, f);
+            done(&a_full[0]);
+            if (!(ok = wait_a(gg, 1))) return;
+#pragma unroll
+            for (int c = 2; c < AC + 1; ++c) put(ast + c * CH, v + 2 * c, f);
+            done(&a_full[1]);
+          }
+        };
+        fetch(va, fa, g);
         for (int u = 0; u < n && ok; u += 2) {
-          if (u + 1 < n) fetch(vb, g + u + 1);
-          if (ok) store(va, g + u, u == 0);
+          if (u + 1 < n) fetch(vb, fb, g + u + 1);
+          if (ok) store(va, fa, g + u, u == 0);
           if (u + 1 < n && ok) {
-            if (u + 2 < n) fetch(va, g + u + 2);
-            if (ok) store(vb, g + u + 1, false);
+            if (u + 2 < n) fetch(va, fa, g + u + 2);
+            if (ok) store(vb, fb, g + u + 1, false);
           }
         }
       } else {
-        // thread: 16 bytes of each of two tokens a chunk, copied without registers
-        const int r = lt >> 3, p = lt & 7;
+        // thread: 16 bytes of each chunk of four tokens, copied without registers
+        const int p = lt & 7, r0 = lt >> 3;
         for (int u = 0; u < n && ok; ++u) {
-          const uint32_t gg = g + u, slot = gg % RR, vs = gg % NVS;
+          const uint32_t gg = g + u, slot = gg % RR;
           ok = wwait(&r_full[slot], (gg / RR) & 1, a.err);
           if (!ok) break;
-          const int ra = rows[slot * NR + r], rb = rows[slot * NR + r + 32];
+          int row[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) row[i] = rows[slot * NR + r0 + 16 * i];
           __syncwarp();
           if (lane == 0) mbar_arrive(&r_empty[slot]);
-          const uint8_t* sa = a.pool + static_cast<size_t>(ra < 0 ? 0 : ra) * (DSA_DIM * 2) + p * 16;
-          const uint8_t* sb = a.pool + static_cast<size_t>(rb < 0 ? 0 : rb) * (DSA_DIM * 2) + p * 16;
-          const int sw = r * 128 + ((p ^ (r & 7)) << 4);             // (r + 32) & 7 == r & 7
-          for (int c = 0; c < 9; ++c) {
-            const int dc = c < 4 ? 4 * (half ^ 1) + c : c == 4 ? 8 : 4 * half + (c - 5);
-            uint8_t* dst;
-            if (c < XC) {
-              const uint32_t x = gg * XC + c, xs = x % XRING;
-              ok = wwait(&x_empty[xs], ((x / XRING) & 1) ^ 1, a.err);
-              dst = xst + xs * CH;
-            } else {
-              if (c == XC) {
-                ok = wwait(&v_empty[vs], ((gg / NVS) & 1) ^ 1, a.err);
-                if (u == 0) ok = ok && wwait(q_ready, seg & 1, a.err);
-              }
-              dst = vst + vs * VC * CH + (c - XC) * CH;
+          auto copy = [&](uint8_t* dst, int dc) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = r0 + 16 * i;                             // r & 7 == r0 & 7
+              cp_async16(dst + r * 128 + ((p ^ (r0 & 7)) << 4),
+                         a.pool + static_cast<size_t>(row[i] < 0 ? 0 : row[i]) * (DSA_DIM * 2) + dc * 128 + p * 16,
+                         row[i] >= 0 ? 16u : 0u);
             }
-            if (!ok) break;
-            cp_async16(dst + sw, sa + dc * 128, ra >= 0 ? 16u : 0u);
-            cp_async16(dst + sw + 32 * 128, sb + dc * 128, rb >= 0 ? 16u : 0u);
-            if (c < XC) cp_async_arrive_noinc(&x_full[(gg * XC + c) % XRING]);
-            if (c == 8) cp_async_arrive_noinc(&v_full[vs]);
+          };
+          if (vals) {
+            // a stage is handed over once the next tile's copies are on their way
+            if (!(ok = wait_v(gg, u == 0))) break;
+#pragma unroll
+            for (int c = 0; c < VC; ++c) copy(vst + (gg % NV) * (VC * CH) + c * CH, 4 * half + c);
+            cp_async_commit();
+            if (u > 0) {
+              cp_async_wait<1>();
+              done(&v_full[(gg - 1) % NV]);
+            }
+          } else {
+            if (!(ok = wait_a(gg, 0))) break;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) copy(ast + c * CH, 4 * (half ^ 1) + c);
+            cp_async_commit();
+            if (!(ok = wait_a(gg, 1))) break;
+#pragma unroll
+            for (int c = 2; c < AC + 1; ++c) copy(ast + c * CH, c < 4 ? 4 * (half ^ 1) + c : 8);
+            cp_async_commit();
+            cp_async_wait<1>();
+            done(&a_full[0]);
+            cp_async_wait<0>();
+            done(&a_full[1]);
           }
+        }
+        if (vals) {
+          cp_async_wait<0>();
+          if (ok) done(&v_full[(g + n - 1) % NV]);
         }
       }
       g += n;
