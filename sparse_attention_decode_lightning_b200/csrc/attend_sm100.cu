@@ -7,13 +7,18 @@
 // (RANGE), or a row of selected positions (IDX).  The cache is bf16, or e4m3
 // codes with an fp32 scale s_j for each block of tokens: C[j] = s_j * code[j].
 //
-// One pass over the list in tiles of 64 tokens.  A CTA owns 256 of the 512
-// value dims and every query head (M = 128; 64 heads leave the upper rows
-// zero), so the scores of a tile are computed by the two CTAs of a pair, and
-// nothing crosses between them: 36 score steps and 16 value steps of 32 and
-// 128 tensor cycles a tile, 1664, where an undivided tile would need 1088 a
-// CTA.  What it saves is an exchange of scores in the middle of each tile's
-// chain, which set the pace of the gathered kernel of sparse_mla_sm100.cu.
+// One pass over the list in tiles of 128 tokens by a cluster of two CTAs and
+// cta_group::2 MMAs (M = 128 over the pair).  A CTA owns half of the heads as
+// accumulator rows, the scores' keys of 64 of the tile's tokens, and 256 of the
+// 512 value dims of all 128, so nothing is computed twice and neither scores
+// nor P cross between the CTAs:
+//   scores  D[64 heads x 128 tokens] a CTA: 36 steps of N = 128
+//   values  D[64 heads x 512 dims]   a CTA: 8 steps of 2 x N = 256
+// 1152 + 1024 tensor cycles a tile, the count of the formula.  Shared memory
+// is read and written at about 120 of its 128 bytes a cycle meanwhile, so a
+// smaller tile, which re-reads the query more often, would be bound by it.
+// With two accumulator halves in the lanes, a head's row of scores lies in two
+// threads (tokens 0..63 and 64..127), which exchange their maxima.
 //
 // The work is cut evenly: the tiles of all queries, one after another, are
 // divided over the SM pairs, so ragged lists leave no pair idle; a query whose
@@ -26,22 +31,28 @@
 // in [2^14, 2^15) and rounded to fp16 (exact for all that is not 2^-28 times
 // smaller), P as fp16.  The scales enter in fp32: z_j takes s_j, and P_j is
 // formed as exp2(z_j + log2 s_j - m) with m the running maximum of that sum,
-// so that P <= 2^8 whatever the scales are; l sums P_j / s_j.  Sums, maxima
+// so that P <= 2^8 whatever the scales are; l sums exp2(z_j - m).  Sums, maxima
 // and O are fp32.
 //
-// Tensor memory (512 columns): O [0,256) | scores slot 0 [256,320) | slot 1
-// [320,384) | the 256 query dims that are also this CTA's value dims [384,512).
-// P overwrites its slot's scores.  Shared memory: the other 320 query dims
-// (80 KB), three stages of value chunks (4 x 8 KB each), one stage of the 5
-// other chunks of a tile, refilled by halves while the tile's values run.  A
-// chunk is 64 tokens x 64 dims, 16 bits, in the 128-byte swizzle.
+// Tensor memory (512 columns): O [0,256), lanes 0..63 dims 0..255 of the CTA's
+// heads, lanes 64..127 dims 256..511 | scores slot 0 [256,320) | slot 1
+// [320,384).  Shared memory: the query (72 KB), P (16 KB), keys as a ring of
+// chunks (64 tokens x 64 dims), values as a ring of slots (16 tokens x 256
+// dims, one MMA step), refilled as soon as their MMAs have read them; all in the
+// 128-byte swizzle.  A bf16 cache's rings hold a whole tile and are filled by
+// gathering TMA loads of four rows.  An e4m3 cache has a tile's codes gathered
+// the same way and widened into shorter rings by eight warps.  TMA carries
+// all gathers: the same loads issued by threads (cp.async, or registers) fill the
+// load/store unit's queue, behind which every barrier and fence of the SM waits;
+// a tile took 10,500 cycles that way, three times its MMAs.
 //
-// Roles (512 threads): warp 0 issues the MMAs; warps 1..3 look up the pool
-// rows (list -> page table -> scale) up to six tiles ahead, since each is a
-// chain of dependent loads; warps 4..7 softmax, rescale and output, one head a
-// thread; warps 8..15 load queries and tiles.  Rows that the list does not
-// hold are filled with zeros and never read, so that what lies in the cache
-// there (NaN, say) cannot reach a product.
+// Roles: warp 0 of the first CTA issues the MMAs of both; warp 1 loads queries
+// and keys, warp 2 values; warp 3 looks up pool rows (list -> page table ->
+// scale), the loads of three tiles under way at once; warps 4..7 softmax,
+// rescale and output, half a head a thread; for an e4m3 cache warps 8..11 widen
+// keys and scale the query, warps 12..15 widen values.  Rows that the list does
+// not hold are gathered from outside the pool, as zeros, and never read, so that
+// what lies in the cache there (NaN, say) cannot reach a product.
 #include "common.cuh"
 #include "internal.h"
 
@@ -51,37 +62,59 @@
 namespace dsa {
 namespace {
 
-constexpr int NR = 64;                               // tokens per tile
-constexpr int CH = NR * 128;                         // chunk bytes: 64 tokens x 64 dims x 2
-constexpr int QCH = 128 * 128;                       // query chunk bytes: 128 heads x 64 dims x 2
-constexpr int AC = 4;                                // latent chunks of a tile that are scores only
-constexpr int VC = 4;                                // chunks that are values too (one more: positions)
-constexpr int NV = 3;                                // value stages
-constexpr int RR = 6;                                // tiles looked up ahead
-constexpr int RESOLVERS = 3;
-constexpr int SMX = 4;                               // softmax warps
-constexpr int GROUP = 4;                             // warps of each of the two loader groups
-constexpr int LOADERS = 2 * GROUP;
-constexpr int THREADS = 32 * (1 + RESOLVERS + SMX + LOADERS);
+constexpr int NT = 128;                              // tokens per tile
+constexpr int NH = NT / 2;                           // of them keys of one CTA
+constexpr int RH = 64;                               // accumulator rows (heads) a CTA
+constexpr int CH = 64 * 128;                         // chunk bytes: 64 rows x 64 dims x 2
+constexpr int KC = DSA_DIM / 64;                     // chunks of a row of 576
+constexpr int VT = 32;                               // tokens of a value unit
+constexpr int VCH = 16 * 128;                        // bytes of 16 tokens x 64 dims
+constexpr int VSTEP = 4 * VCH;                       // and x 256 dims: one MMA step
+constexpr int VSLOT = VT / 16 * VSTEP;
+constexpr int VS = NT / VT;                          // units a tile takes
+constexpr int KU = 3;                                // units of a tile's key codes: 2 of 256 dims, the positions
+constexpr int KUB = NH * 256;                        // bytes of a wide unit
+constexpr int VUB = VT * 256;                        // bytes of a value unit's codes
+constexpr int VUR = 2;                               // units of their ring
+constexpr int RUN = 16;                              // rows that one load can bring where they are consecutive
+constexpr int RR = 3;                                // tiles looked up ahead
+constexpr int SMX = 8;                               // softmax warps
+constexpr int GROUP = 4;                             // warps that widen keys; as many widen values
+constexpr int SMX0 = 4;                              // first of the softmax warps
 
-constexpr int OFF_QX = 0;
-constexpr int OFF_V = OFF_QX + (AC + 1) * QCH;       // [3][4] value chunks
-constexpr int OFF_A = OFF_V + NV * VC * CH;          // [5] chunks of the other half, and the positions
-constexpr int OFF_COL = OFF_A + (AC + 1) * CH;       // float4 [RR][64]: scale, log2 s, 1 / s of each token
-constexpr int OFF_TILE = OFF_COL + RR * NR * 16;     // float4 [RR]: the same for a whole tile; w: it holds
-constexpr int OFF_ROWS = OFF_TILE + RR * 16;         // int32 [RR][64]: pool row or -1
-constexpr int OFF_FOLD = OFF_ROWS + RR * NR * 4;     // uint16 [RR][64]: fp16 factor of a token's codes
-constexpr int OFF_MASK = OFF_FOLD + RR * NR * 2;     // uint32 [RR][2]: tokens that count
-constexpr int OFF_QMUL = OFF_MASK + RR * 2 * 4;      // float [128]
-constexpr int OFF_SCAN = OFF_QMUL + 128 * 4;         // int64 [17], then the first query and its tile
-constexpr int OFF_BAR = OFF_SCAN + 20 * 8;
-constexpr int NBAR = 2 * RR + 4 * 2 + 2 * NV + 3;
-constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
-static_assert(SMEM_BYTES <= 232448, "shared memory exceeds the sm_100 limit");
-static_assert(4 * QCH <= NV * VC * CH, "the query's value-dim chunks pass through the value stages");
-static_assert(OFF_V % 1024 == 0 && OFF_A % 1024 == 0, "swizzle atoms");
-constexpr uint32_t O_COL = 0, S_COL = 256, Q_COL = 384, TMEM_COLS = 512;
+template <bool KV8>
+struct Plan {
+  static constexpr int WARPS = SMX0 + SMX + (KV8 ? 2 * GROUP : 0);
+  static constexpr int THREADS = 32 * WARPS;
+  // A tile's 9 key chunks come in groups, each with its slot: three of three, or
+  // (e4m3) four of two, through two slots, and the positions.
+  static constexpr int KG = KV8 ? 5 : 3;
+  static constexpr int KS = 3;                       // slots
+  static constexpr int KCH = KV8 ? 2 : 3;            // chunks of a slot
+  static constexpr int VR = KV8 ? 2 : 3;             // units of the value ring
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = OFF_Q + KC * CH;
+  static constexpr int OFF_V = OFF_K + (KV8 ? 5 : 9) * CH;
+  static constexpr int OFF_P = OFF_V + VR * VSLOT;   // [2][64 heads x 64 tokens]
+  static constexpr int OFF_KU = OFF_P + 2 * CH;      // e4m3: units of a tile's keys
+  static constexpr int OFF_VU = OFF_KU + (KV8 ? 2 * KUB + NH * 64 : 0);
+  static constexpr int OFF_SCL = OFF_VU + (KV8 ? VUR * VUB : 0);       // e4m3: float [RR][128]: scale of each token
+  static constexpr int OFF_FOLD = OFF_SCL + (KV8 ? RR * NT * 4 : 0);   // half2 [RR][128]: factor of its codes
+  static constexpr int OFF_TILE = OFF_FOLD + (KV8 ? RR * NT * 4 : 0);  // float4 [RR]: scale, log2, 1 / scale of the tile; w: it has one
+  static constexpr int OFF_ROWS = OFF_TILE + (KV8 ? RR * 16 : 0);      // int32 [RR][128]: pool row or -1
+  static constexpr int OFF_MASK = OFF_ROWS + RR * NT * 4;            // uint32 [RR][4]: tokens that count
+  static constexpr int OFF_RUNS = OFF_MASK + RR * 4 * 4;             // uint32 [4]: bit i: rows 16 i .. 16 i + 15 are consecutive, or none is held
+  static constexpr int OFF_QMUL = OFF_RUNS + 16;                     // float [2][64], by segment
+  static constexpr int OFF_MX = OFF_QMUL + 2 * RH * 4;               // float [2][4][64]: between the parts of a row
+  static constexpr int OFF_SCAN = OFF_MX + 8 * RH * 4;               // int64 [20], then the first query and its tile
+  static constexpr int OFF_BAR = OFF_SCAN + 22 * 8;
+  static constexpr int NBAR = 2 * RR + 2 * KS + 2 * VR + 2 + 4 + (KV8 ? 1 + 2 * KU + 2 * VUR : 0);
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16;
+  static_assert(SMEM_BYTES <= 232448, "shared memory exceeds the sm_100 limit");
+  static_assert(WARPS <= 20, "scan");
+};
+constexpr uint32_t O_COL = 0, S_COL = 256, TMEM_COLS = 512;
 
 struct AttendArgs {
   const __nv_bfloat16* q;
@@ -102,11 +135,30 @@ struct AttendArgs {
   float scale_log2;
 };
 
-// first the sinks, then the window of query with `vis` visible tokens
+// pool rows by boxes of one row, for gathers, and of several consecutive ones
+struct AttendMaps {
+  CUtensorMap q;                                     // [Q * H][576], boxes of 64 dims x a CTA's heads
+  CUtensorMap row;                                   // 64 dims (bf16) or 256 codes
+  CUtensorMap run;                                   // bf16: 8 rows x 3 chunks of 64 dims; e4m3: 16 rows x 256 codes
+  CUtensorMap row_pos;                               // e4m3: 64 codes
+  CUtensorMap run_pos;                               // bf16: 16 rows x 4 chunks; e4m3: 16 rows x 64 codes
+};
+
+// The list of a query with `vis` visible tokens, laid out in entries: the
+// sinks, up to a multiple of 16, then the window from a multiple of 16 on, so
+// that 16 entries lie in one page of 16 or more tokens.  Entries that the list
+// does not hold are position -1.
 struct List {
-  int n;            // tokens
-  int ns;           // of them sinks: entry j < ns is position j
-  int w0;           // entry j >= ns is position w0 + j - ns
+  int ns;           // sinks: entry j < ns is position j
+  int ns_pad;
+  int w0;           // first position of the window
+  uint32_t n;       // entries: at most 30 more than tokens
+  __device__ __forceinline__ int position(uint32_t j) const {
+    const uint32_t pad = ns_pad;
+    if (j < pad) return j < static_cast<uint32_t>(ns) ? static_cast<int>(j) : -1;
+    const uint32_t p = (w0 & ~(RUN - 1)) + (j - pad);
+    return j < n && p >= static_cast<uint32_t>(w0) ? static_cast<int>(p) : -1;
+  }
 };
 
 __device__ __forceinline__ int visible(const AttendArgs& a, int q) {
@@ -119,15 +171,17 @@ __device__ __forceinline__ List list_of(const AttendArgs& a, int vis) {
   List l;
   l.ns = min(a.sinks, vis);
   l.w0 = max(l.ns, vis - a.window);
-  l.n = l.ns + vis - l.w0;
+  if (l.w0 == l.ns) l.ns = l.w0 = 0;                 // one range
+  l.ns_pad = l.ns > 0x7FFFFFF0 ? l.ns : (l.ns + RUN - 1) & ~(RUN - 1);
+  l.n = static_cast<uint32_t>(l.ns_pad) + (vis > l.w0 ? vis - (l.w0 & ~(RUN - 1)) : 0);
   return l;
 }
 
 // tiles of query q: at least one, which writes the result of an empty list
 template <bool IDX>
-__device__ __forceinline__ int tiles_of(const AttendArgs& a, int q) {
-  if constexpr (IDX) return (a.topk + NR - 1) / NR;
-  return max(1, (list_of(a, visible(a, q)).n + NR - 1) / NR);
+__device__ __noinline__ int tiles_of(const AttendArgs& a, int q) {
+  if constexpr (IDX) return (a.topk + NT - 1) / NT;
+  return max(1u, (list_of(a, visible(a, q)).n + NT - 1) / NT);
 }
 
 __device__ __forceinline__ int seq_of_query(const int32_t* q_offsets, int B, int q, int lane) {
@@ -143,8 +197,96 @@ __device__ __forceinline__ int seq_of_query(const int32_t* q_offsets, int B, int
   return lo;
 }
 
-__device__ __forceinline__ bool wwait(uint64_t* bar, uint32_t parity, uint32_t* err) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err));
+// Waits of a whole warp for the phase of the given parity, polled and bounded
+// by their number of tries (a try takes about 100 cycles, so they end after
+// about two seconds).  One compact loop: the code of all roles together has to
+// stay in the instruction cache, see below.  NAP: where a late answer costs nothing.
+constexpr uint32_t WAIT_TRIES = 1u << 25;
+template <bool NAP = false>
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, uint32_t* err) {
+#pragma unroll 1
+  for (uint32_t it = 0; !__all_sync(0xffffffffu, mbar_test_wait(bar, parity)); ++it) {
+    if constexpr (NAP) __nanosleep(20);
+    if (it == WAIT_TRIES) {
+      raise_error(err, DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+
+// a ring of N slots: the one in turn, and the parity of its use
+template <int N>
+struct Ring {
+  uint32_t slot = 0, use = 0;
+  __device__ __forceinline__ void next() {
+    if (++slot == N) {
+      slot = 0;
+      use ^= 1;
+    }
+  }
+};
+
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
+               "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+// both CTAs' operands: the same offsets in each one's shared and tensor memory
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrive on `bar` of both CTAs when every MMA issued so far is done
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// Arrive on a barrier of the cluster (its address there) after this CTA's own
+// shared-memory writes, which the fence before has made the tensor core's: the
+// release at cluster scope of mbar_arrive_remote waits for every access under way
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// 16 bytes of shared memory
+__device__ __forceinline__ uint4 lds16(const void* p) { return *static_cast<const uint4*>(p); }
+
+// loads whose bytes count on a barrier of either CTA of the pair
+__device__ __forceinline__ void gather4_pair(void* dst, const CUtensorMap* map, int x, uint4 r, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_2d_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_3d_pair(void* dst, const CUtensorMap* map, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar)
+      : "memory");
 }
 
 __device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
@@ -156,10 +298,18 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// four e4m3 codes -> four fp16 times f (a power of two), exactly
+// four e4m3 codes -> four fp16 times f (a power of two), exactly.  Written in
+// PTX: the intrinsic of the pair type costs twice the instructions.
 __device__ __forceinline__ uint2 widen4(uint32_t w, __half2 f) {
-  const __half2 a = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3)), f);
-  const __half2 b = __hmul2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3)), f);
+  uint2 r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(r.x), "=r"(r.y)
+      : "r"(w));
+  const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&r.x), f);
+  const __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&r.y), f);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
@@ -181,78 +331,122 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t w, float s) {
   return f16x2_bits(__uint_as_float(w << 16) * s, __uint_as_float(w & 0xFFFF0000u) * s);
 }
 
+// 16 codes of a token, widened: pieces p and p + 1 of the 128-byte row dst, whose
+// swizzle is sw; `flip` stores the second first
+__device__ __forceinline__ void store_wide(uint8_t* dst, int p, int sw, int flip, uint4 c, __half2 f) {
+  const uint2 w0 = widen4(c.x, f), w1 = widen4(c.y, f), w2 = widen4(c.z, f), w3 = widen4(c.w, f);
+  const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
+  *reinterpret_cast<uint4*>(dst + (((p + flip) ^ sw) << 4)) = flip ? hi : lo;
+  *reinterpret_cast<uint4*>(dst + (((p + 1 - flip) ^ sw) << 4)) = flip ? lo : hi;
+}
+
+// first row of a run: of rows that the list does not hold, all before the pool
+__device__ __forceinline__ int run_start(int row) { return row < 0 ? -RUN : row; }
+
+// e4m3: 16 rows of a tile: in one box where they are consecutive, else in boxes of four
+__device__ __forceinline__ void load_rows(uint8_t* dst, int step, const CUtensorMap* row, const CUtensorMap* run_map,
+                                          int x, const int* r, bool run, uint32_t bar, bool lead) {
+  if (run) {
+    const int r0 = run_start(*r);
+    if (lead) load_2d_pair(dst, run_map, x, r0, bar);
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < RUN / 4; ++i) {
+      const uint4 v = lds16(r + 4 * i);
+      if (lead) gather4_pair(dst + i * step, row, x, v, bar);
+    }
+  }
+  __syncwarp();
+}
+
 template <bool KV8, bool IDX>
-__global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constant__ AttendArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint8_t* qx = smem + OFF_QX;
-  uint8_t* vst = smem + OFF_V;
-  uint8_t* ast = smem + OFF_A;
-  int* rows = reinterpret_cast<int*>(smem + OFF_ROWS);
-  float4* col = reinterpret_cast<float4*>(smem + OFF_COL);
-  float4* tsc = reinterpret_cast<float4*>(smem + OFF_TILE);
-  uint16_t* fold = reinterpret_cast<uint16_t*>(smem + OFF_FOLD);
-  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + OFF_MASK);
-  float* qmul = reinterpret_cast<float*>(smem + OFF_QMUL);
-  int64_t* scan = reinterpret_cast<int64_t*>(smem + OFF_SCAN);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+__global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
+    attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ AttendMaps maps) {
+  using L = Plan<KV8>;
+  constexpr int THREADS = L::THREADS, KG = L::KG, KS = L::KS, KCH = L::KCH, VR = L::VR;
+  extern __shared__ __align__(1024) uint8_t smem[];  // the swizzle's atoms: 1024 bytes
+  uint8_t* qs = smem + L::OFF_Q;
+  uint8_t* ks = smem + L::OFF_K;
+  uint8_t* vs = smem + L::OFF_V;
+  uint8_t* ps = smem + L::OFF_P;
+  float* scl = reinterpret_cast<float*>(smem + L::OFF_SCL);
+  __half2* fold = reinterpret_cast<__half2*>(smem + L::OFF_FOLD);
+  float4* tsc = reinterpret_cast<float4*>(smem + L::OFF_TILE);
+  int* rows = reinterpret_cast<int*>(smem + L::OFF_ROWS);
+  uint32_t* mask = reinterpret_cast<uint32_t*>(smem + L::OFF_MASK);
+  uint32_t* runs = reinterpret_cast<uint32_t*>(smem + L::OFF_RUNS);
+  float* qmul = reinterpret_cast<float*>(smem + L::OFF_QMUL);
+  float* mx = reinterpret_cast<float*>(smem + L::OFF_MX);
+  int64_t* scan = reinterpret_cast<int64_t*>(smem + L::OFF_SCAN);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::OFF_BAR);
+  // "full" barriers of the MMAs' operands are the first CTA's, fed by both;
+  // the MMAs arrive on both CTAs' "empty" ones
   uint64_t* r_full = bars;                 // [RR] rows of a tile are looked up
   uint64_t* r_empty = r_full + RR;
-  uint64_t* a_full = r_empty + RR;         // [2] chunks 0, 1 of a tile, then 2, 3 and the positions
-  uint64_t* a_empty = a_full + 2;          // [2] the scores have read them
-  uint64_t* s_full = a_empty + 2;          // [2] scores of a tile are in their slot
-  uint64_t* p_full = s_full + 2;           // [2] P of a tile is in its slot
-  uint64_t* v_full = p_full + 2;           // [NV] a tile's value chunks
-  uint64_t* v_free = v_full + NV;          // [NV] the value MMA is done: its stage and scores slot are free
-  uint64_t* q_staged = v_free + NV;        // a segment's query is in shared memory
-  uint64_t* q_ready = q_staged + 1;        // ... and its value dims in tensor memory
-  uint64_t* o_final = q_ready + 1;         // every MMA of a segment is done
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  uint64_t* k_full = r_empty + RR;         // [KS]
+  uint64_t* k_empty = k_full + KS;
+  uint64_t* v_full = k_empty + KS;         // [VR]
+  uint64_t* v_empty = v_full + VR;
+  uint64_t* s_full = v_empty + VR;         // [2] scores of a tile are in their slot
+  uint64_t* p_full = s_full + 2;           // P of a tile is in shared memory
+  uint64_t* pv_done = p_full + 1;          // its value MMAs are done: P is free, O holds
+  uint64_t* q_full = pv_done + 1;          // a segment's query is in shared memory
+  uint64_t* q_empty = q_full + 1;          // its scores are done
+  uint64_t* q_raw = q_empty + 1;           // e4m3: this CTA's part as bf16
+  uint64_t* ku_full = q_raw + 1;           // e4m3: [3] units of key codes
+  uint64_t* ku_empty = ku_full + KU;
+  uint64_t* vu_full = ku_empty + KU;       // e4m3: [2] units of value codes
+  uint64_t* vu_empty = vu_full + VUR;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int half = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int HC = a.H >> 1;                           // this CTA's heads: 64 or 32
+  const int live_smx = a.H == 128 ? SMX : SMX / 2;   // warps whose rows hold heads
   pdl_trigger();
+  if (tid == 32) {
+    tma_prefetch_desc(&maps.q);
+    tma_prefetch_desc(&maps.row);
+    tma_prefetch_desc(&maps.run);
+    if (KV8) {
+      tma_prefetch_desc(&maps.row_pos);
+      tma_prefetch_desc(&maps.run_pos);
+    }
+  }
 
-  if (tid == 0) {
-    for (int i = 0; i < RR; ++i) {
-      mbar_init(&r_full[i], 1);
-      mbar_init(&r_empty[i], LOADERS + SMX);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&a_full[i], GROUP);
-      mbar_init(&a_empty[i], 1);
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], SMX);
-    }
-    for (int i = 0; i < NV; ++i) {
-      mbar_init(&v_full[i], GROUP);
-      mbar_init(&v_free[i], 1);
-    }
-    mbar_init(q_staged, LOADERS);
-    mbar_init(q_ready, SMX);
-    mbar_init(o_final, 1);
+  if (tid < L::NBAR) {
+    // arrivals a phase: one, but for these
+    const int i = tid;
+    const int full = KV8 ? 2 * GROUP : 1;            // widened operands: a warp each
+    int n = 1;
+    if (i >= RR && i < 2 * RR) n = 2 + live_smx + (KV8 ? 2 * GROUP : 0);
+    if (i >= k_full - bars && i < k_empty - bars) n = full;
+    if (i >= v_full - bars && i < v_empty - bars) n = full;
+    if (i == p_full - bars) n = 2 * live_smx;
+    if (i == q_full - bars) n = full;
+    if (KV8 && ((i >= ku_empty - bars && i < vu_full - bars) || i >= vu_empty - bars)) n = GROUP;
+    mbar_init(bars + i, n);
     mbar_fence_init();
   }
-  if (warp == 0) tmem_alloc(tmem_holder, TMEM_COLS);
+  if (warp == 0) tmem_alloc_pair(tmem_holder, TMEM_COLS);
 
   // This pair's share [t0, t1) of all tiles: a thread sums the tiles of some
   // consecutive queries, the block scans the sums.
   const int per = (a.Q + THREADS - 1) / THREADS;
   const int qa = min(a.Q, tid * per), qb = min(a.Q, qa + per);
   int64_t sum = 0;
+#pragma unroll 1
   for (int q = qa; q < qb; ++q) sum += tiles_of<IDX>(a, q);
   int64_t incl = sum;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) scan[warp] = incl;
-  tc_fence_before();
   __syncthreads();
-  tc_fence_after();
   int64_t base = 0, total = 0;
+#pragma unroll 1
   for (int w = 0; w < THREADS / 32; ++w) {
     if (w == warp) base = total;
     total += scan[w];
@@ -264,144 +458,302 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
   if (t1 > t0 && t0 >= base && t0 < base + sum) {
     int64_t at = base;
     int q = qa;
+#pragma unroll 1
     for (int n; at + (n = tiles_of<IDX>(a, q)) <= t0; ++q) at += n;
-    scan[17] = q;
-    scan[18] = t0 - at;
+    scan[20] = q;
+    scan[21] = t0 - at;
   }
   if (half == 0 && tid < 2 && t1 == t0) a.desc[2 * pair + tid] = -1;
-  __syncthreads();
+  tc_fence_before();
+  cluster_sync();                                    // both CTAs' barriers and tensor memory are there
+  tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int q0 = static_cast<int>(scan[17]);
-  const int off0 = static_cast<int>(scan[18]);
+  const int q0 = static_cast<int>(scan[20]);
+  const int off0 = static_cast<int>(scan[21]);
   const int ntile = static_cast<int>(t1 - t0);
+
+  // the first CTA's barrier of the same name
+  auto leader = [&](uint64_t* bar) { return map_to_rank(smem_u32(bar), 0); };
+  // a warp's part of an operand is written: tell the MMA issuer
+  auto hand_over = [&](uint64_t* bar) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_pair(leader(bar));
+    __syncwarp();
+  };
+  // slot of a tile's key group j, and the parity of its use: slots 0 and 1 of an
+  // e4m3 tile are used twice
+  auto key_slot = [](int j) { return KV8 ? (j == 4 ? 2 : j & 1) : j; };
+  auto key_use = [](int j, uint32_t g) { return KV8 && j < 4 ? static_cast<uint32_t>(j >> 1) : g & 1; };
+  // the query of a segment, once the scores of the one before are done
+  auto load_query = [&](int q, uint32_t seg, bool lead) {
+    if (seg > 0 && !await<true>(q_empty, (seg - 1) & 1, a.err)) return false;
+    if (lead) {
+      const uint32_t bytes = static_cast<uint32_t>(KC * 128 * HC);
+      const uint32_t bar = KV8 ? smem_u32(q_raw) : leader(q_full);
+      if (KV8) mbar_arrive_expect_tx(q_raw, bytes);
+      else if (half == 0) mbar_arrive_expect_tx(q_full, 2 * bytes);
+#pragma unroll 1
+      for (int c = 0; c < KC; ++c) load_2d_pair(qs + c * CH, &maps.q, 64 * c, q * a.H + half * HC, bar);
+    }
+    __syncwarp();
+    return true;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ MMA issuer
     // The warp walks together, so that descriptors stay in uniform registers,
-    // and one elected lane issues.  The loaders fence their own writes.
+    // and one elected lane issues.
     constexpr uint32_t fmt = KV8 ? 0u /*F16*/ : 1u /*BF16*/;
-    constexpr uint32_t idesc_s = umma_idesc(fmt, 128, NR);
+    constexpr uint32_t idesc_s = umma_idesc(fmt, 128, NT);
     constexpr uint32_t idesc_pv = umma_idesc(fmt, 128, 256, 0, 1);
-    const uint64_t dq = umma_desc_sw128(smem_u32(qx), 1024, 16);
-    const uint64_t da = umma_desc_sw128(smem_u32(ast), 1024, 16);
-    const uint64_t dv = umma_desc_sw128(smem_u32(vst), 1024, 16);
-    const uint64_t dm = umma_desc_sw128_mn(smem_u32(vst), CH, 1024);
+    const uint64_t dq = umma_desc_sw128(smem_u32(qs), 1024, 16);
+    const uint64_t dk = umma_desc_sw128(smem_u32(ks), KV8 ? 1024 : 1024 * KCH, 16);
+    const uint64_t dp = umma_desc_sw128(smem_u32(ps), 1024, 16);
+    const uint64_t dv = umma_desc_sw128_mn(smem_u32(vs), VCH, 1024);
     const bool lead = elect_one();
     bool ok = true;
-    int q = q0, off = off0, left = ntile;
+    int q = q0, off = off0, left = half == 0 ? ntile : 0;
     uint32_t g = 0;                              // tiles so far
+    Ring<VR> vr;
+#pragma unroll 1
     for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
       const int n = min(tiles_of<IDX>(a, q) - off, left);
       left -= n;
-      if (!(ok = wwait(q_ready, seg & 1, a.err))) break;
-      tc_fence_after();
-      // values of tile u - 1 between the scores of tile u, so that neither the
-      // softmax before nor the free slot after is waited for
+      if (!(ok = await(q_full, seg & 1, a.err))) break;
+      // the scores of tile u before the values of tile u - 1, so that the
+      // softmax of each runs beside MMAs
+#pragma unroll 1
       for (int u = 0; u <= n && ok; ++u) {
-        const uint32_t gu = g + u, sb = gu & 1, vs = gu % NV;
-        const uint32_t d = tmem + S_COL + sb * NR;
+        const uint32_t gu = g + u;
         if (u < n) {
-          // P of tile u - 2 has left the slot
-          if (gu >= 2 && !(ok = wwait(&v_free[(gu - 2) % NV], ((gu - 2) / NV) & 1, a.err))) break;
-          if (!(ok = wwait(&a_full[0], gu & 1, a.err))) break;
-          tc_fence_after();
-          if (lead) {
+          const uint32_t d = tmem + S_COL + (gu & 1) * NH;
+#pragma unroll 1
+          for (int j = 0; j < KG; ++j) {
+            const int slot = key_slot(j), nc = KV8 && j == 4 ? 1 : KCH;
+            if (!(ok = await(&k_full[slot], key_use(j, gu), a.err))) break;
+            tc_fence_after();
+            if (lead) {
+#pragma unroll 1
+              for (int c = 0; c < nc; ++c) {
+                const uint64_t dqc = dq + (KCH * j + c) * (CH >> 4), dkc = dk + (KCH * slot * CH + c * (KV8 ? CH : 1024)) / 16;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16(d, dq + (k >> 2) * (QCH >> 4) + (k & 3) * 2, da + (k >> 2) * (CH >> 4) + (k & 3) * 2, idesc_s,
-                      k > 0);
-            mma_commit(&a_empty[0]);
+                for (int k = 0; k < 4; ++k)
+                  mma_f16_pair(d, dqc + k * 2, dkc + k * 2, idesc_s, j > 0 || c > 0 || k > 0 ? 1u : 0u);
+              }
+              mma_commit_pair(&k_empty[slot]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
-          if (!(ok = wwait(&a_full[1], gu & 1, a.err))) break;
-          tc_fence_after();
+          if (!ok) break;
           if (lead) {
-#pragma unroll
-            for (int k = 8; k < 4 * (AC + 1); ++k)
-              mma_f16(d, dq + (k >> 2) * (QCH >> 4) + (k & 3) * 2, da + (k >> 2) * (CH >> 4) + (k & 3) * 2, idesc_s,
-                      1u);
-            mma_commit(&a_empty[1]);
-          }
-          __syncwarp();
-          if (!(ok = wwait(&v_full[vs], (gu / NV) & 1, a.err))) break;
-          tc_fence_after();
-          if (lead) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16_ts(d, tmem + Q_COL + k * 8, dv + vs * (VC * CH >> 4) + (k >> 2) * (CH >> 4) + (k & 3) * 2,
-                         idesc_s, 1u);
+            mma_commit_pair(&s_full[gu & 1]);
+            if (u == n - 1) mma_commit_pair(q_empty);
           }
           __syncwarp();
         }
         if (u >= 1) {
-          const uint32_t gt = gu - 1, tb = gt & 1, ts = gt % NV;
-          if (!(ok = wwait(&p_full[tb], (gt >> 1) & 1, a.err))) break;
-          tc_fence_after();
-          if (lead) {
+          if (!(ok = await(p_full, (gu - 1) & 1, a.err))) break;
+#pragma unroll 1
+          for (int i = 0; i < VS; ++i) {
+            if (!(ok = await(&v_full[vr.slot], vr.use, a.err))) break;
+            tc_fence_after();
+            if (lead) {
 #pragma unroll
-            for (int k = 0; k < NR / 16; ++k)
-              mma_f16_ts(tmem + O_COL, tmem + S_COL + tb * NR + k * 8, dm + ts * (VC * CH >> 4) + k * (2048 >> 4),
-                         idesc_pv, (u > 1 || k > 0) ? 1u : 0u);
-            mma_commit(&v_free[ts]);
-            if (u == n) mma_commit(o_final);
+              for (int k = 0; k < VT / 16; ++k) {
+                const uint64_t dpi = dp + (i >> 1) * (CH >> 4) + (i & 1) * 4 + k * 2;
+                const uint64_t dvi = dv + vr.slot * (VSLOT >> 4) + k * (VSTEP >> 4);
+                const uint32_t acc = u > 1 || i > 0 || k > 0 ? 1u : 0u;
+                mma_f16_pair(tmem + O_COL, dpi, dvi, idesc_pv, acc);
+                mma_f16_pair(tmem + O_COL + 128, dpi, dvi + (2 * VCH >> 4), idesc_pv, acc);
+              }
+              mma_commit_pair(&v_empty[vr.slot]);
+            }
+            __syncwarp();
+            vr.next();
           }
-          __syncwarp();
-        }
-        if (u < n) {
-          if (lead) {
-#pragma unroll
-            for (int k = 8; k < 4 * VC; ++k)
-              mma_f16_ts(d, tmem + Q_COL + k * 8, dv + vs * (VC * CH >> 4) + (k >> 2) * (CH >> 4) + (k & 3) * 2,
-                         idesc_s, 1u);
-            mma_commit(&s_full[sb]);
-          }
+          if (!ok) break;
+          if (lead) mma_commit_pair(pv_done);
           __syncwarp();
         }
       }
       g += n;
     }
-  } else if (warp < 1 + RESOLVERS) {
-    // ------------------------------------------------------------ row look-up
+  } else if (KV8 && warp == 1) {
+    // ------------------------------------------------------------ e4m3: queries, key codes
+    const bool lead = elect_one();
     bool ok = true;
     int q = q0, off = off0, left = ntile;
     uint32_t g = 0;
-    while (left > 0 && ok) {
+#pragma unroll 1
+    for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
       const int n = min(tiles_of<IDX>(a, q) - off, left);
       left -= n;
-      const int b = seq_of_query(a.q_offsets, a.B, q, lane);
-      const int vis = visible(a, q);
-      if (__ldg(a.q_vis + q) > vis && lane == 0) raise_error(a.err, DEVERR_BOUNDS);
-      const List ls = list_of(a, vis);
-      for (int u = 0; u < n; ++u, ++g) {
-        if (g % RESOLVERS != static_cast<uint32_t>(warp - 1)) continue;
+#pragma unroll 1
+      for (int u = 0; u < n && ok; ++u, ++g) {
         const uint32_t slot = g % RR;
-        int row[2];
-        float s[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int j = (off + u) * NR + 32 * i + lane;
-          int pos = -1;
-          if constexpr (IDX) {
-            if (j < a.topk) pos = __ldg(a.idx + static_cast<size_t>(q) * a.topk + j);
-          } else {
-            if (j < ls.n) pos = j < ls.ns ? j : ls.w0 + (j - ls.ns);
-          }
-          row[i] = -1;
-          s[i] = 1.f;
-          if (pos >= 0 && pos < vis) {
-            const int pg = __ldg(a.page_table + static_cast<size_t>(b) * a.max_pages + (pos >> a.page_shift));
-            if (pg >= 0 && pg < a.num_pages) {
-              row[i] = (pg << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
-              if constexpr (KV8) {
-                s[i] = __ldg(a.kv_scales + (row[i] >> a.block_shift));
-                if (!(s[i] >= 0x1p-40f && s[i] <= 0x1p40f)) row[i] = -1;
+        if (!(ok = await<true>(&r_full[slot], (g / RR) & 1, a.err))) break;
+        const uint32_t run = runs[slot] >> (half * (NH / RUN));
+        const int* r = rows + slot * NT + half * NH;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          if (!(ok = await<true>(&ku_empty[c], (g & 1) ^ 1, a.err))) break;
+          if (lead) mbar_arrive_expect_tx(&ku_full[c], KUB);
+#pragma unroll 1
+          for (int i = 0; i < NH / RUN; ++i)
+            load_rows(smem + L::OFF_KU + c * KUB + i * RUN * 256, 1024, &maps.row, &maps.run, 256 * c, r + i * RUN,
+                      (run >> i) & 1u, smem_u32(&ku_full[c]), lead);
+        }
+        if (!(ok = ok && await<true>(&ku_empty[2], (g & 1) ^ 1, a.err))) break;
+        if (lead) mbar_arrive_expect_tx(&ku_full[2], NH * 64);
+#pragma unroll 1
+        for (int i = 0; i < NH / RUN; ++i)
+          load_rows(smem + L::OFF_KU + 2 * KUB + i * RUN * 64, 256, &maps.row_pos, &maps.run_pos, DSA_DIM_V, r + i * RUN,
+                    (run >> i) & 1u, smem_u32(&ku_full[2]), lead);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&r_empty[slot]);
+        __syncwarp();
+        if (u == 0) ok = load_query(q, seg, lead);   // its keys are on their way
+      }
+    }
+  } else if (KV8 && warp == 2) {
+    // ------------------------------------------------------------ e4m3: value codes
+    const bool lead = elect_one();
+    bool ok = true;
+    Ring<VUR> ur;
+#pragma unroll 1
+    for (int g = 0; g < ntile && ok; ++g) {
+      const uint32_t slot = g % RR;
+      if (!(ok = await<true>(&r_full[slot], (g / RR) & 1, a.err))) break;
+      const uint32_t run = runs[slot];
+#pragma unroll 1
+      for (int c = 0; c < VS; ++c) {
+        if (!(ok = await<true>(&vu_empty[ur.slot], ur.use ^ 1, a.err))) break;
+        if (lead) mbar_arrive_expect_tx(&vu_full[ur.slot], VUB);
+#pragma unroll 1
+        for (int i = 0; i < VT / RUN; ++i)
+          load_rows(smem + L::OFF_VU + ur.slot * VUB + i * RUN * 256, 1024, &maps.row, &maps.run, 256 * half,
+                    rows + slot * NT + c * VT + i * RUN, (run >> (2 * c + i)) & 1u, smem_u32(&vu_full[ur.slot]), lead);
+        ur.next();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&r_empty[slot]);
+      __syncwarp();
+    }
+  } else if (!KV8 && warp == 1) {
+    // ------------------------------------------------------------ bf16: queries, keys
+    // A load takes about 45 cycles to issue whatever its size, so its box is as
+    // large as consecutive rows allow.  A slot holds 8 rows x 3 chunks after
+    // another; rows that are apart come by fours, a chunk at a time.
+    const bool lead = elect_one();
+    bool ok = true;
+    int q = q0, off = off0, left = ntile;
+    uint32_t g = 0;
+#pragma unroll 1
+    for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
+      const int n = min(tiles_of<IDX>(a, q) - off, left);
+      left -= n;
+#pragma unroll 1
+      for (int u = 0; u < n && ok; ++u, ++g) {
+        const uint32_t slot = g % RR;
+        if (!(ok = await<true>(&r_full[slot], (g / RR) & 1, a.err))) break;
+        const uint32_t run = runs[slot] >> (half * (NH / RUN));
+        const int* r = rows + slot * NT + half * NH;
+#pragma unroll 1
+        for (int j = 0; j < KG; ++j) {
+          if (!(ok = await<true>(&k_empty[j], (g & 1) ^ 1, a.err))) break;
+          const uint32_t bar = leader(&k_full[j]);
+          if (half == 0 && lead) mbar_arrive_expect_tx(&k_full[j], 2 * KCH * CH);
+#pragma unroll 1
+          for (int i = 0; i < NH / RUN; ++i) {
+            uint8_t* dst = ks + j * KCH * CH + i * 2 * KCH * 1024;
+            if ((run >> i) & 1u) {
+              const int r0 = run_start(r[i * RUN]);
+              if (lead) {
+                load_3d_pair(dst, &maps.run, r0, KCH * j, bar);
+                load_3d_pair(dst + KCH * 1024, &maps.run, r0 + 8, KCH * j, bar);
+              }
+            } else {
+#pragma unroll 1
+              for (int t = 0; t < RUN / 4 * KCH; ++t) {
+                const int c = t >> 2, p = t & 3;
+                const uint4 v = lds16(r + i * RUN + 4 * p);
+                if (lead)
+                  gather4_pair(dst + (p >> 1) * KCH * 1024 + c * 1024 + (p & 1) * 512, &maps.row, 64 * (KCH * j + c), v, bar);
               }
             }
+            __syncwarp();
           }
-          if (row[i] < 0 && pos != -1) raise_error(a.err, DEVERR_BOUNDS);
         }
-        ok = wwait(&r_empty[slot], ((g / RR) & 1) ^ 1, a.err);
-        if (!ok) break;
+        if (lane == 0) mbar_arrive(&r_empty[slot]);
+        __syncwarp();
+        if (u == 0 && ok) ok = load_query(q, seg, lead);   // its keys are on their way
+      }
+    }
+    // the MMAs have read every key, so no load is under way
+#pragma unroll 1
+    for (int j = 0; j < KG && ok && ntile > 0; ++j) ok = await<true>(&k_empty[j], (ntile - 1) & 1, a.err);
+  } else if (!KV8 && warp == 2) {
+    // ------------------------------------------------------------ bf16: values
+    const bool lead = elect_one();
+    bool ok = true;
+    Ring<VR> vr;
+#pragma unroll 1
+    for (int g = 0; g < ntile && ok; ++g) {
+      const uint32_t slot = g % RR;
+      if (!(ok = await<true>(&r_full[slot], (g / RR) & 1, a.err))) break;
+      uint32_t run = runs[slot];
+      const int* r = rows + slot * NT;
+#pragma unroll 1
+      for (int i = 0; i < VS; ++i, r += VT) {
+        if (!(ok = await<true>(&v_empty[vr.slot], vr.use ^ 1, a.err))) break;
+        const uint32_t bar = leader(&v_full[vr.slot]);
+        if (half == 0 && lead) mbar_arrive_expect_tx(&v_full[vr.slot], 2 * VSLOT);
+#pragma unroll 1
+        for (int j = 0; j < VT / RUN; ++j, run >>= 1) {
+          uint8_t* dst = vs + vr.slot * VSLOT + j * VSTEP;
+          if (run & 1u) {
+            const int r0 = run_start(r[j * RUN]);
+            if (lead) load_3d_pair(dst, &maps.run_pos, r0, 4 * half, bar);
+          } else {
+#pragma unroll 1
+            for (int t = 0; t < RUN; ++t) {
+              const int c = t >> 2, p = t & 3;
+              const uint4 v = lds16(r + j * RUN + 4 * p);
+              if (lead) gather4_pair(dst + c * VCH + p * 512, &maps.row, 256 * half + 64 * c, v, bar);
+            }
+          }
+          __syncwarp();
+        }
+        vr.next();
+      }
+      if (lane == 0) mbar_arrive(&r_empty[slot]);
+      __syncwarp();
+    }
+#pragma unroll 1
+    for (int i = 0; i < VR && ok && ntile > 0; ++i) {
+      ok = await<true>(&v_empty[vr.slot], vr.use ^ 1, a.err);
+      vr.next();
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ row look-up
+    // Three dependent loads a token (selected position, page, scale), of which
+    // each step of the loop issues one for each of three tiles.
+    bool ok = true, bad = false;
+    int q = q0 - 1, off = 0, n = 0, left = ntile, u = 0;
+    int b = 0, vis = 0;
+    List ls = {};
+    int pos[4], at[4], pg[4], row[4];                // tile i; tile i - 1; tile i - 2
+    float s[4];
+    int b1 = 0, vis1 = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) pos[k] = at[k] = pg[k] = row[k] = -1;
+#pragma unroll 1
+    for (int i = 0; i < ntile + 3 && ok; ++i) {
+      if (i >= 3) {
+        // tile i - 3: hand it over
+        const uint32_t g = i - 3, slot = g % RR;
+        if (!(ok = await<true>(&r_empty[slot], ((g / RR) & 1) ^ 1, a.err))) break;
         if constexpr (KV8) {
           // Scales that differ by powers of two, up to 2^15, go into the fp16
           // codes, exactly (a code is a multiple of 2^-9, fp16's least step is
@@ -409,9 +761,13 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           // one a token.
           uint32_t lo = 0xffffffffu, hi = 0, mlo = 0xffffffffu, mhi = 0;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t bits = __float_as_uint(s[i]);
-            if (row[i] >= 0) {
+          for (int k = 0; k < 4; ++k) {
+            if (row[k] >= 0 && !(s[k] >= 0x1p-40f && s[k] <= 0x1p40f)) {
+              row[k] = -1;
+              bad = true;
+            }
+            if (row[k] >= 0) {
+              const uint32_t bits = __float_as_uint(s[k]);
               lo = min(lo, bits);
               hi = max(hi, bits);
               mlo = min(mlo, bits & 0x7FFFFFu);
@@ -423,100 +779,130 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           mlo = __reduce_min_sync(0xffffffffu, mlo);
           mhi = __reduce_max_sync(0xffffffffu, mhi);
           const bool one = hi == 0 || (mlo == mhi && (hi - lo) >> 23 <= 15);
-          const float st = hi == 0 ? 1.f : __uint_as_float(hi);
-          if (lane == 0)
-            tsc[slot] = make_float4(st * a.scale_log2, log2f(st), __fdiv_rn(1.f, st), one ? 1.f : 0.f);
+          const float st = hi == 0 ? 1.f : __uint_as_float(hi), inv = __fdiv_rn(1.f, st);
+          if (lane == 0) tsc[slot] = make_float4(st * a.scale_log2, log2f(st), inv, one ? 1.f : 0.f);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t down = one && row[i] >= 0 ? (hi - __float_as_uint(s[i])) >> 23 : 0u;
-            fold[slot * NR + 32 * i + lane] = down < 15 ? static_cast<uint16_t>((15 - down) << 10) : uint16_t{0x200};
-            if (!one)
-              col[slot * NR + 32 * i + lane] =
-                  row[i] < 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
-                             : make_float4(s[i] * a.scale_log2, log2f(s[i]), __fdiv_rn(1.f, s[i]), 0.f);
+          for (int k = 0; k < 4; ++k) {
+            if (row[k] < 0) s[k] = st;
+            scl[slot * NT + 32 * k + lane] = s[k];
+            fold[slot * NT + 32 * k + lane] = __float2half2_rn(one ? s[k] * inv : 1.f);
           }
         }
+        uint32_t run = 0;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          rows[slot * NR + 32 * i + lane] = row[i];
-          const uint32_t m = __ballot_sync(0xffffffffu, row[i] >= 0);
-          if (lane == 0) mask[slot * 2 + i] = m;
+        for (int k = 0; k < 4; ++k) {
+          rows[slot * NT + 32 * k + lane] = row[k];
+          const uint32_t m = __ballot_sync(0xffffffffu, row[k] >= 0);
+          if (lane == 0) mask[slot * 4 + k] = m;
+          const int first = __shfl_sync(0xffffffffu, row[k], lane & 16);
+          const uint32_t c =
+              __ballot_sync(0xffffffffu, first >= 0 ? row[k] == first + (lane & 15) : row[k] < 0);
+          run |= ((c & 0xFFFFu) == 0xFFFFu ? 1u : 0u) << (2 * k) | (c >> 16 == 0xFFFFu ? 2u : 0u) << (2 * k);
         }
+        if (lane == 0) runs[slot] = run;
         __syncwarp();
         if (lane == 0) mbar_arrive(&r_full[slot]);
+        __syncwarp();
       }
-      ++q;
-      off = 0;
+      // tile i - 2: its pages are here; tile i - 1: its positions are here
+      // (before the first and behind the last tile these are -1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        row[k] = -1;
+        if (pg[k] >= 0 && pg[k] < a.num_pages) row[k] = (pg[k] << a.page_shift) + (at[k] & ((1 << a.page_shift) - 1));
+        bad |= at[k] >= 0 && row[k] < 0;
+        if constexpr (KV8) s[k] = row[k] >= 0 ? __ldg(a.kv_scales + (row[k] >> a.block_shift)) : 1.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        at[k] = pos[k] >= 0 && pos[k] < vis1 ? pos[k] : -1;
+        bad |= at[k] != pos[k] && pos[k] != -1;
+        pg[k] = at[k] >= 0 ? __ldg(a.page_table + static_cast<size_t>(b1) * a.max_pages + (at[k] >> a.page_shift)) : -1;
+      }
+      if (i < ntile && u == n) {
+        ++q;
+        off = i == 0 ? off0 : 0;
+        n = min(tiles_of<IDX>(a, q) - off, left);
+        left -= n;
+        u = 0;
+        b = seq_of_query(a.q_offsets, a.B, q, lane);
+        vis = visible(a, q);
+        bad |= __ldg(a.q_vis + q) > vis;
+        ls = list_of(a, vis);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t j = static_cast<uint32_t>(off + u) * NT + 32 * k + lane;
+        pos[k] = -1;
+        if (i < ntile) {
+          if constexpr (IDX) {
+            if (j < static_cast<uint32_t>(a.topk)) pos[k] = __ldg(a.idx + static_cast<size_t>(q) * a.topk + j);
+          } else {
+            pos[k] = ls.position(j);
+          }
+        }
+      }
+      b1 = b;
+      vis1 = vis;
+      ++u;
     }
-  } else if (warp < 1 + RESOLVERS + SMX) {
+    if (bad) raise_error(a.err, DEVERR_BOUNDS);
+    __syncwarp();
+  } else if (warp < SMX0 + SMX) {
     // ------------------------------------------------------------ softmax, output
-    const int quarter = warp & 3;
-    const int h = quarter * 32 + lane;
+    // thread: accumulator row r, the tile's tokens 64 hh + 32 cg .. + 31, and
+    // value dims 256 hh + 128 cg .. + 127; part = 2 hh + cg
+    const int quarter = warp & 3, hh = quarter >> 1, cg = (warp - SMX0) >> 2;
+    const int r = (quarter & 1) * 32 + lane;
+    const int h = half * HC + r;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t row_bar = 1 + (quarter & 1);      // the four warps of the same rows
     bool ok = true;
-    int q = q0, off = off0, left = ntile;
+    int q = q0, off = off0, left = r < HC ? ntile : 0;
     uint32_t g = 0;
     int head_q = -1, tail_q = -1;                    // queries this pair holds a part of
-    for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
+#pragma unroll 1
+    for (uint32_t seg = 0; left > 0; ++seg, ++q, off = 0) {
       const int nt = tiles_of<IDX>(a, q);
       const int n = min(nt - off, left);
       left -= n;
-      // the query's value dims, staged by the loaders, go to tensor memory
-      ok = wwait(q_staged, seg & 1, a.err);
-      for (int c = 0; c < VC; ++c) {
-        float w[32];
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          const uint4 v = *reinterpret_cast<const uint4*>(vst + c * QCH + h * 128 + ((p ^ (h & 7)) << 4));
-          w[4 * p] = __uint_as_float(v.x);
-          w[4 * p + 1] = __uint_as_float(v.y);
-          w[4 * p + 2] = __uint_as_float(v.z);
-          w[4 * p + 3] = __uint_as_float(v.w);
-        }
-        tmem_st32(lane_base + Q_COL + c * 32, w);
-      }
-      const float qm = KV8 ? qmul[h] : 1.f;
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_ready);
-
-      float m_use = -INFINITY, l = 0.f;
+      float qm = 1.f, m_use = -INFINITY, l = 0.f;
+#pragma unroll 1
       for (int u = 0; u < n; ++u, ++g) {
         const uint32_t sb = g & 1, slot = g % RR;
-        if (ok) ok = wwait(&r_full[slot], (g / RR) & 1, a.err);
-        if (ok) ok = wwait(&s_full[sb], (g >> 1) & 1, a.err);
+        if (ok) ok = await(&r_full[slot], (g / RR) & 1, a.err);
+        const uint32_t live = mask[slot * 4 + 2 * hh + cg];
+        if (ok) ok = await(&s_full[sb], (g >> 1) & 1, a.err);
         tc_fence_after();
-        float z[NR];
-        tmem_ld32(lane_base + S_COL + sb * NR, z);
-        tmem_ld32(lane_base + S_COL + sb * NR + 32, z + 32);
+        float z[32];
+        tmem_ld32(lane_base + S_COL + sb * NH + cg * 32, z);
+        // the scores are there, so the query's factors are
+        if (KV8 && u == 0) qm = qmul[(seg & 1) * RH + r];
         tmem_ld_wait();
-        const uint32_t m0 = mask[slot * 2], m1 = mask[slot * 2 + 1];
-        const float4* cp = col + slot * NR;
+        float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         float4 ts = make_float4(a.scale_log2, 0.f, 1.f, 1.f);
         if constexpr (KV8) ts = tsc[slot];
-        if (!KV8 || ts.w != 0.f) {
+        const bool one = !KV8 || ts.w != 0.f;
+        const float* sc = scl + slot * NT + hh * NH + cg * 32;
+        if (one) {
           const float k = ts.x * qm;
 #pragma unroll
-          for (int j = 0; j < NR; ++j) z[j] = fmaf(z[j], k, ts.y);
+          for (int j = 0; j < 32; ++j) z[j] = fmaf(z[j], k, ts.y);
         } else {
 #pragma unroll
-          for (int j = 0; j < NR; ++j) {
-            const float2 k = *reinterpret_cast<const float2*>(cp + j);
-            z[j] = fmaf(z[j] * qm, k.x, k.y);
-          }
+          for (int j = 0; j < 32; ++j) z[j] = fmaf(z[j] * qm, sc[j] * a.scale_log2, __log2f(sc[j]));
         }
-        if ((m0 & m1) != 0xffffffffu) {
+        if (live != 0xffffffffu) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            z[j] = ((m0 >> j) & 1u) ? z[j] : -INFINITY;
-            z[32 + j] = ((m1 >> j) & 1u) ? z[32 + j] : -INFINITY;
-          }
+          for (int j = 0; j < 32; ++j) z[j] = ((live >> j) & 1u) ? z[j] : -INFINITY;
         }
-        float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < NR; ++j) mt[j & 3] = fmaxf(mt[j & 3], z[j]);
-        const float mtile = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+        for (int j = 0; j < 32; ++j) mt[j & 3] = fmaxf(mt[j & 3], z[j]);
+        float mtile = fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3]));
+        float* mxs = mx + (g & 1) * 4 * RH + r;
+        mxs[(2 * hh + cg) * RH] = mtile;
+        named_barrier(row_bar, 128);
+        mtile = fmaxf(fmaxf(mxs[0], mxs[RH]), fmaxf(mxs[2 * RH], mxs[3 * RH]));
         // the maximum that P refers to moves only when it falls 8 behind (a
         // factor of 2^8, which fp16 holds), so O is seldom rescaled
         float alpha = 1.f;
@@ -529,279 +915,242 @@ __global__ void __launch_bounds__(THREADS, 1) attend_kernel(const __grid_constan
           m_use = mtile;
         }
         const float m_eff = m_use == -INFINITY ? 0.f : m_use;
-        float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          float* zh = z + 32 * hh;
+        for (int j = 0; j < 32; ++j) z[j] = fast_exp2(z[j] - m_eff);
+        if (one) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) zh[j] = fast_exp2(zh[j] - m_eff);
-          if (!KV8 || ts.w != 0.f) {
+          for (int j = 0; j < 32; ++j) sums[j & 3] += z[j];
+        } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) ps[j & 3] += zh[j];
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) ps[j & 3] = fmaf(zh[j], cp[32 * hh + j].z, ps[j & 3]);
-          }
-          float pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            pk[j] = __uint_as_float(KV8 ? f16x2_bits(zh[2 * j], zh[2 * j + 1]) : bf16x2_bits(zh[2 * j], zh[2 * j + 1]));
-          tmem_st16(lane_base + S_COL + sb * NR + 16 * hh, pk);
+          for (int j = 0; j < 32; ++j) sums[j & 3] += __fdividef(z[j], sc[j]);
         }
-        l = fmaf(l, alpha, ((ps[0] + ps[1]) + (ps[2] + ps[3])) * (KV8 && ts.w != 0.f ? ts.z : 1.f));
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&r_empty[slot]);
+        l = fmaf(l, alpha, ((sums[0] + sums[1]) + (sums[2] + sums[3])) * (KV8 && one ? ts.z : 1.f));
+        // the value MMAs of the tile before have read P and written O
+        if (ok && g > 0) ok = await(pv_done, (g - 1) & 1, a.err);
+        uint8_t* pr = ps + hh * CH + r * 128;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float* zj = z + 8 * j;
+          const uint4 w = KV8 ? make_uint4(f16x2_bits(zj[0], zj[1]), f16x2_bits(zj[2], zj[3]), f16x2_bits(zj[4], zj[5]),
+                                           f16x2_bits(zj[6], zj[7]))
+                              : make_uint4(bf16x2_bits(zj[0], zj[1]), bf16x2_bits(zj[2], zj[3]),
+                                           bf16x2_bits(zj[4], zj[5]), bf16x2_bits(zj[6], zj[7]));
+          *reinterpret_cast<uint4*>(pr + (((4 * cg + j) ^ (r & 7)) << 4)) = w;
+        }
         if (__any_sync(0xffffffffu, resc)) {
-          // after the value MMA of the tile before
-          if (ok) ok = wwait(&v_free[(g - 1) % NV], ((g - 1) / NV) & 1, a.err);
           tc_fence_after();
-          for (int c = 0; c < 8; ++c) {
-            float o[32];
-            tmem_ld32(lane_base + O_COL + c * 32, o);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32(lane_base + O_COL + cg * 128 + c * 32, z);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= alpha;
-            tmem_st32(lane_base + O_COL + c * 32, o);
+            for (int i = 0; i < 32; ++i) z[i] *= alpha;
+            tmem_st32(lane_base + O_COL + cg * 128 + c * 32, z);
           }
+          tmem_st_wait();
         }
-        tmem_st_wait();
         tc_fence_before();
+        hand_over(p_full);
+        if (lane == 0) mbar_arrive(&r_empty[slot]);  // only now: the stores have waited for the loads
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[sb]);
       }
       // ---- the segment's result: the query's own, or a part of it
-      if (ok) ok = wwait(o_final, seg & 1, a.err);
+      float* mxs = mx + (g & 1) * 4 * RH + r;        // free: the tile before last used it
+      mxs[(2 * hh + cg) * RH] = l;
+      named_barrier(row_bar, 128);
+      l = (mxs[0] + mxs[RH]) + (mxs[2 * RH] + mxs[3 * RH]);
+      named_barrier(row_bar, 128);
+      if (ok) ok = await(pv_done, (g - 1) & 1, a.err);
       tc_fence_after();
       const bool whole = n == nt;
       const bool head = off == 0;
       const int part = 2 * pair + (head ? 1 : 0);
       if (!whole) (head ? head_q : tail_q) = q;
-      const bool live = h < a.H;
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // NaN stays NaN
       const bool none = l == 0.f;
-      for (int c = 0; c < 8; ++c) {
+      const int d0 = 256 * hh + 128 * cg;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
         float o[32];
-        tmem_ld32(lane_base + O_COL + c * 32, o);
+        tmem_ld32(lane_base + O_COL + cg * 128 + c * 32, o);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * inv;
-        if (!live) continue;
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(q) * a.H + h) * DSA_DIM_V + 256 * half + 32 * c);
+          uint4* dst = reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(q) * a.H + h) * DSA_DIM_V + d0 + 32 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             dst[i] = make_uint4(bf16x2_bits(o[8 * i], o[8 * i + 1]), bf16x2_bits(o[8 * i + 2], o[8 * i + 3]),
                                 bf16x2_bits(o[8 * i + 4], o[8 * i + 5]), bf16x2_bits(o[8 * i + 6], o[8 * i + 7]));
         } else {
-          float4* dst = reinterpret_cast<float4*>(a.o_part + (static_cast<size_t>(part) * a.H + h) * DSA_DIM_V + 256 * half + 32 * c);
+          float4* dst = reinterpret_cast<float4*>(a.o_part + (static_cast<size_t>(part) * a.H + h) * DSA_DIM_V + d0 + 32 * c);
 #pragma unroll
           for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
-      if (half == 0 && live)
+      if (hh == 0 && cg == 0)
         (whole ? a.lse + static_cast<size_t>(q) * a.H + h : a.l_part + static_cast<size_t>(part) * a.H + h)[0] =
             none ? -INFINITY : (m_use + log2f(l)) * 0.69314718055994531f;
       tc_fence_before();                             // O was read before the next segment writes it
     }
-    if (half == 0 && quarter == 0 && lane == 0 && ntile > 0) {
+    if (half == 0 && warp == SMX0 && lane == 0 && ntile > 0) {
       a.desc[2 * pair] = tail_q;
       a.desc[2 * pair + 1] = head_q;
     }
-  } else {
-    // ------------------------------------------------------------ loaders
-    // Two groups of four warps, so that neither waits for the other's stage:
-    // group 0 fills the scores-only chunks (one stage, handed over in halves),
-    // group 1 the value chunks (three stages).
-    const int lw = warp - (1 + RESOLVERS + SMX);
-    const bool vals = lw >= GROUP;
-    const int lt = (lw & (GROUP - 1)) * 32 + lane;
+    __syncwarp();
+  } else if (KV8 && warp < SMX0 + SMX + GROUP) {
+    // ------------------------------------------------------------ e4m3: keys widened, queries scaled
+    // Two chunks at a time.  thread: 16 codes of four tokens; the lanes of the
+    // upper chunk store their two pieces in the other order, so that the eight
+    // lanes of a store lie in different banks.
+    const int lw = warp - (SMX0 + SMX);
+    const int lt = lw * 32 + lane;
+    const int pc = lt & 7, r0 = lt >> 3, flip = pc >> 2;
+    const int pp = lt & 3, rp = lt >> 2;             // the positions: 16 codes of two tokens
     bool ok = true;
     int q = q0, off = off0, left = ntile;
     uint32_t g = 0;
+
+    // The query as fp16 in place, each head scaled so that its largest element
+    // lies in [2^14, 2^15); infinities and NaN stay what they are.  A warp takes
+    // a quarter of the heads, two at a time; 72 pieces of 8 dims a head.
+    auto query = [&](uint32_t seg) {
+      if (!(ok = ok && await(q_raw, seg & 1, a.err))) return;
+#pragma unroll 1
+      for (int h0 = (HC >> 2) * lw; h0 < (HC >> 2) * (lw + 1); h0 += 2) {
+        uint4 v[2][3];
+        auto piece = [&](int r, int k) {
+          const int p = 32 * k + lane;
+          return reinterpret_cast<uint4*>(qs + (p >> 3) * CH + r * 128 + (((p & 7) ^ (r & 7)) << 4));
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int k = 0; k < 3; ++k) v[i][k] = k < 2 || lane < 8 ? *piece(h0 + i, k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int k = 0; k < 3; ++k) m = mag2(mag2(mag2(mag2(m, v[i][k].x), v[i][k].y), v[i][k].z), v[i][k].w);
+          m = max(m & 0xFFFFu, m >> 16);
+          m = __reduce_max_sync(0xffffffffu, m);
+          const int e = min(max(static_cast<int>(m >> 7), 14), 254);
+          const float s = m == 0 || m >= 0x7F80u ? 1.f : __uint_as_float(static_cast<uint32_t>(min(254, 268 - e)) << 23);
+#pragma unroll
+          for (int k = 0; k < 3; ++k)
+            if (k < 2 || lane < 8)
+              *piece(h0 + i, k) = make_uint4(scale_pair(v[i][k].x, s), scale_pair(v[i][k].y, s),
+                                             scale_pair(v[i][k].z, s), scale_pair(v[i][k].w, s));
+          if (lane == 0) qmul[(seg & 1) * RH + h0 + i] = __fdiv_rn(1.f, s);
+        }
+      }
+      hand_over(q_full);
+      __syncwarp();
+    };
+
+#pragma unroll 1
     for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
       const int n = min(tiles_of<IDX>(a, q) - off, left);
       left -= n;
-      if (seg > 0) ok = wwait(o_final, (seg - 1) & 1, a.err);
-      if (!ok) break;
-      // the query: a warp takes 16 heads, four at a time; 72 pieces of 8 dims
-      // a head.  Chunks of this CTA's value dims pass through the value stages.
-      for (int h0 = 16 * lw; h0 < 16 * lw + 16; h0 += 4) {
-        uint4 v[4][3];
+#pragma unroll 1
+      for (int u = 0; u < n && ok; ++u, ++g) {
+        const uint32_t slot = g % RR;
+        if (!(ok = await(&r_full[slot], (g / RR) & 1, a.err))) break;
+        const __half2* fs = fold + slot * NT + half * NH;
+        __half2 f[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4* src = reinterpret_cast<const uint4*>(a.q + (static_cast<size_t>(q) * a.H + h0 + i) * DSA_DIM);
+        for (int i = 0; i < 4; ++i) f[i] = fs[r0 + 16 * i];
+#pragma unroll 1
+        for (int d = 0; d < 4; ++d) {
+          if (u == 0 && d == 2) query(seg);          // both slots are full: their scores wait for the query
+          if ((d & 1) == 0) ok = ok && await(&ku_full[d >> 1], g & 1, a.err);
+          const uint8_t* src = smem + L::OFF_KU + (d >> 1) * KUB + (d & 1) * 128 + pc * 16;
+          uint4 v[4];
 #pragma unroll
-          for (int k = 0; k < 3; ++k)
-            v[i][k] = h0 + i < a.H && (k < 2 || lane < 8) ? __ldg(src + 32 * k + lane) : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < 4; ++i) v[i] = lds16(src + (r0 + 16 * i) * 256);
+          if (!(ok = ok && await(&k_empty[d & 1], key_use(d, g) ^ 1, a.err))) break;
+          uint8_t* dst = ks + (2 * (d & 1) + flip) * CH + r0 * 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) store_wide(dst + i * 16 * 128, 2 * (pc & 3), r0 & 7, flip, v[i], f[i]);
+          hand_over(&k_full[d & 1]);
+          if ((d & 1) && lane == 0) mbar_arrive(&ku_empty[d >> 1]);   // only now: the stores have waited for the loads
+          __syncwarp();
         }
+        ok = ok && await(&ku_full[2], g & 1, a.err);
+        uint4 v[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int h = h0 + i;
-          if constexpr (KV8) {
-            uint32_t m = 0;
+        for (int i = 0; i < 2; ++i) v[i] = lds16(smem + L::OFF_KU + 2 * KUB + (rp + 32 * i) * 64 + pp * 16);
+        if (!(ok = ok && await(&k_empty[2], (g & 1) ^ 1, a.err))) break;
 #pragma unroll
-            for (int k = 0; k < 3; ++k) m = mag2(mag2(mag2(mag2(m, v[i][k].x), v[i][k].y), v[i][k].z), v[i][k].w);
-            m = max(m & 0xFFFFu, m >> 16);
-            m = __reduce_max_sync(0xffffffffu, m);
-            // largest element in [2^14, 2^15); infinities and NaN stay what they are
-            const int e = min(max(static_cast<int>(m >> 7), 14), 254);
-            const float s = m == 0 || m >= 0x7F80u ? 1.f : __uint_as_float(static_cast<uint32_t>(min(254, 268 - e)) << 23);
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-              v[i][k] = make_uint4(scale_pair(v[i][k].x, s), scale_pair(v[i][k].y, s), scale_pair(v[i][k].z, s),
-                                   scale_pair(v[i][k].w, s));
-            if (lane == 0) qmul[h] = __fdiv_rn(1.f, s);
-          }
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            if (k == 2 && lane >= 8) continue;
-            const int p = 32 * k + lane, c = p >> 3;
-            const int sw = h * 128 + (((p & 7) ^ (h & 7)) << 4);
-            const int x = c == 8 ? AC : (c & 3);
-            uint8_t* dst = c < 8 && (c >> 2) == half ? vst + (c & 3) * QCH : qx + x * QCH;
-            *reinterpret_cast<uint4*>(dst + sw) = v[i][k];
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_staged);
-
-      auto wait_a = [&](uint32_t gg, int part) { return wwait(&a_empty[part], (gg & 1) ^ 1, a.err); };
-      auto wait_v = [&](uint32_t gg, bool first) {
-        if (first && !wwait(q_ready, seg & 1, a.err)) return false;   // the query has left the stages
-        return wwait(&v_free[gg % NV], ((gg / NV) & 1) ^ 1, a.err);
-      };
-      auto done = [&](uint64_t* bar) {                               // the writes are for the tensor core
-        fence_proxy_async_smem();
+        for (int i = 0; i < 2; ++i) store_wide(ks + 4 * CH + (rp + 32 * i) * 128, 2 * pp, rp & 7, 0, v[i], fs[rp + 32 * i]);
+        hand_over(&k_full[2]);
+        if (lane == 0) mbar_arrive(&ku_empty[2]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-      };
-      if constexpr (KV8) {
-        // thread: 16 + 16 codes of each chunk of one token; a tile's pieces are
-        // all in flight before the tile before is widened and stored.  The
-        // rows of a quarter warp, r & 7 in {0,1,4,5} or {2,3,6,7}, put its 16-byte
-        // stores into eight different bank groups.
-        const int rj = lt >> 1, u2 = lt & 1;
-        const int r = (rj & ~7) | (rj & 1) | ((rj & 2) << 1) | ((rj & 4) >> 1);
-        uint4 va[2 * (AC + 1)], vb[2 * (AC + 1)];
-        __half2 fa, fb;
-        auto fetch = [&](uint4* v, __half2& f, uint32_t gg) {
-          const uint32_t slot = gg % RR;
-          ok = ok && wwait(&r_full[slot], (gg / RR) & 1, a.err);
-          const int row = ok ? rows[slot * NR + r] : -1;
-          f = __half2half2(__ushort_as_half(fold[slot * NR + r]));
-          const uint4* src = reinterpret_cast<const uint4*>(a.pool + static_cast<size_t>(row < 0 ? 0 : row) * DSA_DIM) + u2;
-          const int c0 = 4 * (vals ? half : half ^ 1);
-#pragma unroll
-          for (int c = 0; c < AC + 1; ++c) {
-            const int dc = c < 4 ? c0 + c : 8;
-            const bool get = row >= 0 && (c < 4 || !vals);
-            v[2 * c] = get ? __ldg(src + 4 * dc) : make_uint4(0u, 0u, 0u, 0u);
-            v[2 * c + 1] = get ? __ldg(src + 4 * dc + 2) : make_uint4(0u, 0u, 0u, 0u);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&r_empty[slot]);
-        };
-        // pieces 2 u2 + {0, 1} and 4 + 2 u2 + {0, 1} of token r's 128 bytes
-        auto put = [&](uint8_t* dst, const uint4* v, __half2 f) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint2 a0 = widen4(v[i].x, f), a1 = widen4(v[i].y, f), a2 = widen4(v[i].z, f), a3 = widen4(v[i].w, f);
-            const int p = 4 * i + 2 * u2;
-            *reinterpret_cast<uint4*>(dst + r * 128 + ((p ^ (r & 7)) << 4)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
-            *reinterpret_cast<uint4*>(dst + r * 128 + (((p + 1) ^ (r & 7)) << 4)) = make_uint4(a2.x, a2.y, a3.x, a3.y);
-          }
-        };
-        auto store = [&](const uint4* v, __half2 f, uint32_t gg, bool first) {
-          if (vals) {
-            if (!(ok = wait_v(gg, first))) return;
-#pragma unroll
-            for (int c = 0; c < VC; ++c) put(vst + (gg % NV) * (VC * CH) + c * CH, v + 2 * c, f);
-            done(&v_full[gg % NV]);
-          } else {
-            if (!(ok = wait_a(gg, 0))) return;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) put(ast + c * CH, v + 2 * c, f);
-            done(&a_full[0]);
-            if (!(ok = wait_a(gg, 1))) return;
-#pragma unroll
-            for (int c = 2; c < AC + 1; ++c) put(ast + c * CH, v + 2 * c, f);
-            done(&a_full[1]);
-          }
-        };
-        fetch(va, fa, g);
-        for (int u = 0; u < n && ok; u += 2) {
-          if (u + 1 < n) fetch(vb, fb, g + u + 1);
-          if (ok) store(va, fa, g + u, u == 0);
-          if (u + 1 < n && ok) {
-            if (u + 2 < n) fetch(va, fa, g + u + 2);
-            if (ok) store(vb, fb, g + u + 1, false);
-          }
-        }
-      } else {
-        // thread: 16 bytes of each chunk of four tokens, copied without registers
-        const int p = lt & 7, r0 = lt >> 3;
-        for (int u = 0; u < n && ok; ++u) {
-          const uint32_t gg = g + u, slot = gg % RR;
-          ok = wwait(&r_full[slot], (gg / RR) & 1, a.err);
-          if (!ok) break;
-          int row[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) row[i] = rows[slot * NR + r0 + 16 * i];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&r_empty[slot]);
-          auto copy = [&](uint8_t* dst, int dc) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = r0 + 16 * i;                             // r & 7 == r0 & 7
-              cp_async16(dst + r * 128 + ((p ^ (r0 & 7)) << 4),
-                         a.pool + static_cast<size_t>(row[i] < 0 ? 0 : row[i]) * (DSA_DIM * 2) + dc * 128 + p * 16,
-                         row[i] >= 0 ? 16u : 0u);
-            }
-          };
-          if (vals) {
-            // a stage is handed over once the next tile's copies are on their way
-            if (!(ok = wait_v(gg, u == 0))) break;
-#pragma unroll
-            for (int c = 0; c < VC; ++c) copy(vst + (gg % NV) * (VC * CH) + c * CH, 4 * half + c);
-            cp_async_commit();
-            if (u > 0) {
-              cp_async_wait<1>();
-              done(&v_full[(gg - 1) % NV]);
-            }
-          } else {
-            if (!(ok = wait_a(gg, 0))) break;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) copy(ast + c * CH, 4 * (half ^ 1) + c);
-            cp_async_commit();
-            if (!(ok = wait_a(gg, 1))) break;
-#pragma unroll
-            for (int c = 2; c < AC + 1; ++c) copy(ast + c * CH, c < 4 ? 4 * (half ^ 1) + c : 8);
-            cp_async_commit();
-            cp_async_wait<1>();
-            done(&a_full[0]);
-            cp_async_wait<0>();
-            done(&a_full[1]);
-          }
-        }
-        if (vals) {
-          cp_async_wait<0>();
-          if (ok) done(&v_full[(g + n - 1) % NV]);
-        }
+        if (lane == 0) mbar_arrive(&r_empty[slot]);
+        __syncwarp();
       }
-      g += n;
     }
-    cp_async_wait<0>();                              // nothing in flight when the CTA retires
+    // the MMAs have read every key
+    if (ok && ntile > 0)
+      ok = await<true>(&k_empty[0], 1, a.err) && await<true>(&k_empty[1], 1, a.err) &&
+           await<true>(&k_empty[2], (ntile - 1) & 1, a.err);
+  } else if (KV8) {
+    // ------------------------------------------------------------ e4m3: values widened
+    // A unit at a time.  thread: 16 codes of four tokens; lanes of odd chunks
+    // store their two pieces in the other order, as above.
+    const int lt = (warp - (SMX0 + SMX + GROUP)) * 32 + lane;
+    const int pc = lt & 15, r0 = lt >> 4, flip = (pc >> 2) & 1;
+    bool ok = true;
+    Ring<VR> vr;
+    Ring<VUR> ur;
+#pragma unroll 1
+    for (int g = 0; g < ntile && ok; ++g) {
+      const uint32_t slot = g % RR;
+      if (!(ok = await(&r_full[slot], (g / RR) & 1, a.err))) break;
+      const __half2* fs = fold + slot * NT + r0;
+#pragma unroll 1
+      for (int c = 0; c < VS; ++c, fs += VT) {
+        ok = await(&vu_full[ur.slot], ur.use, a.err);
+        const uint8_t* src = smem + L::OFF_VU + ur.slot * VUB + r0 * 256 + pc * 16;
+        uint4 v[4];
+        __half2 f[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = lds16(src + i * 8 * 256);
+          f[i] = fs[8 * i];
+        }
+        if (!(ok = ok && await(&v_empty[vr.slot], vr.use ^ 1, a.err))) break;
+        uint8_t* dst = vs + vr.slot * VSLOT + (pc >> 2) * VCH + r0 * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          store_wide(dst + (i >> 1) * VSTEP + (i & 1) * 1024, 2 * (pc & 3), r0 & 7, flip, v[i], f[i]);
+        hand_over(&v_full[vr.slot]);
+        if (lane == 0) mbar_arrive(&vu_empty[ur.slot]);
+        __syncwarp();
+        vr.next();
+        ur.next();
+      }
+      if (lane == 0) mbar_arrive(&r_empty[slot]);
+      __syncwarp();
+    }
+    // the MMAs have read every value
+#pragma unroll 1
+    for (int i = 0; i < VR && ok && ntile > 0; ++i) {
+      ok = await<true>(&v_empty[vr.slot], vr.use ^ 1, a.err);
+      vr.next();
+    }
   }
 
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    tmem_dealloc_pair(tmem, TMEM_COLS);
   }
 }
+
 
 // Merge of the parts of queries whose tiles lie on several pairs: pair p holds
 // the first part of query desc[2p + 1] in part 2p + 1, the pairs after it the
@@ -848,15 +1197,26 @@ constexpr size_t L_OFF = DESC_OFF + 2 * MAX_PAIRS * 4 + 176;      // 1024
 static_assert(L_OFF % 256 == 0, "aligned");
 
 template <bool KV8, bool IDX>
-cudaError_t launch(const AttendArgs& a, int pairs, cudaStream_t st) {
+cudaError_t launch(const AttendArgs& a, const AttendMaps& m, int pairs, cudaStream_t st) {
   static std::atomic<bool> done[64];
   auto kernel = attend_kernel<KV8, IDX>;
   const cudaError_t e = set_once_per_device(done, [kernel] {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Plan<KV8>::SMEM_BYTES);
   });
   if (e != cudaSuccess) return e;
-  kernel<<<2 * pairs, THREADS, SMEM_BYTES, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
+  cfg.blockDim = dim3(Plan<KV8>::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Plan<KV8>::SMEM_BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, m);
 }
 
 }  // namespace
@@ -899,8 +1259,25 @@ cudaError_t launch_attend(const __nv_bfloat16* q, const void* pool, const float*
   a.scale_log2 = scale * 1.4426950408889634f;
   const int sms = device_sm_count() / 2;
   const int pairs = sms < 1 ? 1 : (sms < MAX_PAIRS ? sms : MAX_PAIRS);
-  cudaError_t e = idx ? launch<true, true>(a, pairs, st)
-                      : (kv_scales ? launch<true, false>(a, pairs, st) : launch<false, false>(a, pairs, st));
+  AttendMaps m = {};
+  const uint64_t pool_rows = static_cast<uint64_t>(num_pages) * page_size;
+  const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  bool ok = encode_tiled_2d(&m.q, bf, q, DSA_DIM, static_cast<uint64_t>(Q) * H, DSA_DIM * 2, 64, H / 2);
+  // boxes of several rows are used where the rows are consecutive
+  if (kv_scales) {
+    const CUtensorMapSwizzle flat = CU_TENSOR_MAP_SWIZZLE_NONE;
+    ok = ok && encode_tiled_2d(&m.row, u8, pool, DSA_DIM, pool_rows, DSA_DIM, 256, 1, flat) &&
+         encode_tiled_2d(&m.run, u8, pool, DSA_DIM, pool_rows, DSA_DIM, 256, RUN, flat) &&
+         encode_tiled_2d(&m.row_pos, u8, pool, DSA_DIM, pool_rows, DSA_DIM, 64, 1, flat) &&
+         encode_tiled_2d(&m.run_pos, u8, pool, DSA_DIM, pool_rows, DSA_DIM, 64, RUN, flat);
+  } else {
+    ok = ok && encode_tiled_2d(&m.row, bf, pool, DSA_DIM, pool_rows, DSA_DIM * 2, 64, 1) &&
+         encode_chunks_bf16(&m.run, pool, KC, pool_rows, DSA_DIM * 2, 8, 3) &&
+         encode_chunks_bf16(&m.run_pos, pool, KC, pool_rows, DSA_DIM * 2, RUN, 4);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  cudaError_t e = idx ? launch<true, true>(a, m, pairs, st)
+                      : (kv_scales ? launch<true, false>(a, m, pairs, st) : launch<false, false>(a, m, pairs, st));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(H / 4), 1);

@@ -34,7 +34,13 @@ struct WsLayout {
 // 2-D tensor map, 128-byte swizzle, no OOB fill value (zeros)
 bool encode_tiled_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                      uint64_t inner_elems, uint64_t rows, uint64_t row_stride_bytes,
-                     uint32_t box_inner, uint32_t box_rows);
+                     uint32_t box_inner, uint32_t box_rows,
+                     CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
+
+// bf16 rows as chunks of 64 elements: a 3-D map (element, row, chunk), so that
+// a box of rows x chunks lands chunk after chunk, each in the 128-byte swizzle
+bool encode_chunks_bf16(CUtensorMap* map, const void* base, uint64_t chunks, uint64_t rows,
+                        uint64_t row_stride_bytes, uint32_t box_rows, uint32_t box_chunks);
 
 // Runs `set` (cudaFuncSetAttribute calls) once per device and remembers the
 // success in `done` (device ids below 64; other ids run `set` on every call).
