@@ -79,12 +79,12 @@ constexpr int VUR = 2;                               // units of their ring
 constexpr int RUN = 16;                              // rows that one load can bring where they are consecutive
 constexpr int RR = 3;                                // tiles looked up ahead
 constexpr int SMX = 8;                               // softmax warps
-constexpr int GROUP = 4;                             // warps that widen keys; as many widen values
+constexpr int CONV = 8;                               // warps that widen codes
 constexpr int SMX0 = 4;                              // first of the softmax warps
 
 template <bool KV8>
 struct Plan {
-  static constexpr int WARPS = SMX0 + SMX + (KV8 ? 2 * GROUP : 0);
+  static constexpr int WARPS = SMX0 + SMX + (KV8 ? CONV : 0);
   static constexpr int THREADS = 32 * WARPS;
   // A tile's 9 key chunks come in groups, each with its slot: three of three, or
   // (e4m3) four of two, through two slots, and the positions.
@@ -324,8 +324,10 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-// larger magnitude bits of a bf16 pair's two values, seen as two u16
-__device__ __forceinline__ uint32_t mag2(uint32_t m, uint32_t w) { return __vmaxu2(m, w & 0x7FFF7FFFu); }
+// larger of m and the magnitude bits of a bf16 pair's two values
+__device__ __forceinline__ uint32_t mag2(uint32_t m, uint32_t w) {
+  return max(max(m, (w << 16) & 0x7FFF0000u), w & 0x7FFF0000u);
+}
 
 __device__ __forceinline__ uint32_t scale_pair(uint32_t w, float s) {
   return f16x2_bits(__uint_as_float(w << 16) * s, __uint_as_float(w & 0xFFFF0000u) * s);
@@ -340,24 +342,42 @@ __device__ __forceinline__ void store_wide(uint8_t* dst, int p, int sw, int flip
   *reinterpret_cast<uint4*>(dst + (((p + 1 - flip) ^ sw) << 4)) = flip ? lo : hi;
 }
 
-// first row of a run: of rows that the list does not hold, all before the pool
-__device__ __forceinline__ int run_start(int row) { return row < 0 ? -RUN : row; }
-
-// e4m3: 16 rows of a tile: in one box where they are consecutive, else in boxes of four
-__device__ __forceinline__ void load_rows(uint8_t* dst, int step, const CUtensorMap* row, const CUtensorMap* run_map,
-                                          int x, const int* r, bool run, uint32_t bar, bool lead) {
-  if (run) {
-    const int r0 = run_start(*r);
-    if (lead) load_2d_pair(dst, run_map, x, r0, bar);
-  } else {
+// The query as fp16 in place, each head scaled so that its largest element lies
+// in [2^14, 2^15); infinities and NaN stay what they are.  A warp takes an
+// eighth of the heads, two at a time; 72 pieces of 8 dims a head.  A function of
+// its own, since two places call it.
+__device__ __noinline__ void scale_query(uint8_t* qs, float* qmul, int heads, int lw, int lane) {
 #pragma unroll 1
-    for (int i = 0; i < RUN / 4; ++i) {
-      const uint4 v = lds16(r + 4 * i);
-      if (lead) gather4_pair(dst + i * step, row, x, v, bar);
+  for (int h0 = heads * lw; h0 < heads * (lw + 1); h0 += 2) {
+    uint4 v[2][3];
+    auto piece = [&](int r, int k) {
+      const int p = 32 * k + lane;
+      return reinterpret_cast<uint4*>(qs + (p >> 3) * CH + r * 128 + (((p & 7) ^ (r & 7)) << 4));
+    };
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) v[i][k] = k < 2 || lane < 8 ? *piece(h0 + i, k) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) m = mag2(mag2(mag2(mag2(m, v[i][k].x), v[i][k].y), v[i][k].z), v[i][k].w);
+      m = __reduce_max_sync(0xffffffffu, m) >> 16;
+      const int e = min(max(static_cast<int>(m >> 7), 14), 254);
+      const float s = m == 0 || m >= 0x7F80u ? 1.f : __uint_as_float(static_cast<uint32_t>(min(254, 268 - e)) << 23);
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k < 2 || lane < 8)
+          *piece(h0 + i, k) = make_uint4(scale_pair(v[i][k].x, s), scale_pair(v[i][k].y, s), scale_pair(v[i][k].z, s),
+                                         scale_pair(v[i][k].w, s));
+      if (lane == 0) qmul[h0 + i] = __fdiv_rn(1.f, s);
     }
   }
-  __syncwarp();
 }
+
+// first row of a run: of rows that the list does not hold, all before the pool
+__device__ __forceinline__ int run_start(int row) { return row < 0 ? -RUN : row; }
 
 template <bool KV8, bool IDX>
 __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
@@ -417,14 +437,14 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   if (tid < L::NBAR) {
     // arrivals a phase: one, but for these
     const int i = tid;
-    const int full = KV8 ? 2 * GROUP : 1;            // widened operands: a warp each
+    const int full = KV8 ? 2 * CONV : 1;             // widened operands: a warp each
     int n = 1;
-    if (i >= RR && i < 2 * RR) n = 2 + live_smx + (KV8 ? 2 * GROUP : 0);
+    if (i >= RR && i < 2 * RR) n = 2 + live_smx + (KV8 ? CONV : 0);
     if (i >= k_full - bars && i < k_empty - bars) n = full;
     if (i >= v_full - bars && i < v_empty - bars) n = full;
     if (i == p_full - bars) n = 2 * live_smx;
     if (i == q_full - bars) n = full;
-    if (KV8 && ((i >= ku_empty - bars && i < vu_full - bars) || i >= vu_empty - bars)) n = GROUP;
+    if (KV8 && ((i >= ku_empty - bars && i < vu_full - bars) || i >= vu_empty - bars)) n = CONV;
     mbar_init(bars + i, n);
     mbar_fence_init();
   }
@@ -452,9 +472,12 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     total += scan[w];
   }
   base += incl - sum;
-  const int64_t np = total < pairs ? total : pairs;       // pairs that get work
-  const int64_t t0 = pair < np ? total * pair / np : 0;
-  const int64_t t1 = pair < np ? total * (pair + 1) / np : 0;
+  const uint32_t np = total < pairs ? static_cast<uint32_t>(total) : pairs;   // pairs that get work
+  const int64_t each = total >> 32 ? total / np : static_cast<uint32_t>(total) / np;
+  const uint32_t over = static_cast<uint32_t>(total - each * np);
+  const uint32_t up = pair;
+  const int64_t t0 = up < np ? each * up + min(up, over) : 0;
+  const int64_t t1 = up < np ? t0 + each + (up < over ? 1 : 0) : 0;
   if (t1 > t0 && t0 >= base && t0 < base + sum) {
     int64_t at = base;
     int q = qa;
@@ -579,76 +602,17 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       }
       g += n;
     }
-  } else if (KV8 && warp == 1) {
-    // ------------------------------------------------------------ e4m3: queries, key codes
-    const bool lead = elect_one();
-    bool ok = true;
-    int q = q0, off = off0, left = ntile;
-    uint32_t g = 0;
-#pragma unroll 1
-    for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
-      const int n = min(tiles_of<IDX>(a, q) - off, left);
-      left -= n;
-#pragma unroll 1
-      for (int u = 0; u < n && ok; ++u, ++g) {
-        const uint32_t slot = g % RR;
-        if (!(ok = await<true>(&r_full[slot], (g / RR) & 1, a.err))) break;
-        const uint32_t run = runs[slot] >> (half * (NH / RUN));
-        const int* r = rows + slot * NT + half * NH;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          if (!(ok = await<true>(&ku_empty[c], (g & 1) ^ 1, a.err))) break;
-          if (lead) mbar_arrive_expect_tx(&ku_full[c], KUB);
-#pragma unroll 1
-          for (int i = 0; i < NH / RUN; ++i)
-            load_rows(smem + L::OFF_KU + c * KUB + i * RUN * 256, 1024, &maps.row, &maps.run, 256 * c, r + i * RUN,
-                      (run >> i) & 1u, smem_u32(&ku_full[c]), lead);
-        }
-        if (!(ok = ok && await<true>(&ku_empty[2], (g & 1) ^ 1, a.err))) break;
-        if (lead) mbar_arrive_expect_tx(&ku_full[2], NH * 64);
-#pragma unroll 1
-        for (int i = 0; i < NH / RUN; ++i)
-          load_rows(smem + L::OFF_KU + 2 * KUB + i * RUN * 64, 256, &maps.row_pos, &maps.run_pos, DSA_DIM_V, r + i * RUN,
-                    (run >> i) & 1u, smem_u32(&ku_full[2]), lead);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&r_empty[slot]);
-        __syncwarp();
-        if (u == 0) ok = load_query(q, seg, lead);   // its keys are on their way
-      }
-    }
-  } else if (KV8 && warp == 2) {
-    // ------------------------------------------------------------ e4m3: value codes
-    const bool lead = elect_one();
-    bool ok = true;
-    Ring<VUR> ur;
-#pragma unroll 1
-    for (int g = 0; g < ntile && ok; ++g) {
-      const uint32_t slot = g % RR;
-      if (!(ok = await<true>(&r_full[slot], (g / RR) & 1, a.err))) break;
-      const uint32_t run = runs[slot];
-#pragma unroll 1
-      for (int c = 0; c < VS; ++c) {
-        if (!(ok = await<true>(&vu_empty[ur.slot], ur.use ^ 1, a.err))) break;
-        if (lead) mbar_arrive_expect_tx(&vu_full[ur.slot], VUB);
-#pragma unroll 1
-        for (int i = 0; i < VT / RUN; ++i)
-          load_rows(smem + L::OFF_VU + ur.slot * VUB + i * RUN * 256, 1024, &maps.row, &maps.run, 256 * half,
-                    rows + slot * NT + c * VT + i * RUN, (run >> (2 * c + i)) & 1u, smem_u32(&vu_full[ur.slot]), lead);
-        ur.next();
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&r_empty[slot]);
-      __syncwarp();
-    }
-  } else if (!KV8 && warp == 1) {
-    // ------------------------------------------------------------ bf16: queries, keys
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ queries, keys
     // A load takes about 45 cycles to issue whatever its size, so its box is as
-    // large as consecutive rows allow.  A slot holds 8 rows x 3 chunks after
-    // another; rows that are apart come by fours, a chunk at a time.
+    // large as consecutive rows allow.  Lane 4 i + t: rows 4 t .. 4 t + 3 of the
+    // 16 rows i, or of a run lane 4 i (bf16: and 4 i + 2) for all.  A slot of the
+    // bf16 keys holds 8 rows x 3 chunks after another.
     const bool lead = elect_one();
     bool ok = true;
     int q = q0, off = off0, left = ntile;
     uint32_t g = 0;
+    if (ntile > 0) load_query(q, 0, lead);
 #pragma unroll 1
     for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
       const int n = min(tiles_of<IDX>(a, q) - off, left);
@@ -657,83 +621,99 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       for (int u = 0; u < n && ok; ++u, ++g) {
         const uint32_t slot = g % RR;
         if (!(ok = await<true>(&r_full[slot], (g / RR) & 1, a.err))) break;
-        const uint32_t run = runs[slot] >> (half * (NH / RUN));
-        const int* r = rows + slot * NT + half * NH;
+        const bool run = (runs[slot] >> (half * (NH / RUN) + (lane >> 2 & 3))) & 1u;
+        const uint4 r = lds16(rows + slot * NT + half * NH + 4 * (lane & 15));
+        const int r0 = run_start(static_cast<int>(r.x));
+        const int i = lane >> 2, t = lane & 3;
 #pragma unroll 1
-        for (int j = 0; j < KG; ++j) {
-          if (!(ok = await<true>(&k_empty[j], (g & 1) ^ 1, a.err))) break;
-          const uint32_t bar = leader(&k_full[j]);
-          if (half == 0 && lead) mbar_arrive_expect_tx(&k_full[j], 2 * KCH * CH);
+        for (int j = 0; j < 3; ++j) {
+          uint64_t* full = KV8 ? &ku_full[j] : &k_full[j];
+          if (!(ok = await<true>(KV8 ? &ku_empty[j] : &k_empty[j], (g & 1) ^ 1, a.err))) break;
+          if constexpr (KV8) {
+            const int pitch = j < 2 ? 256 : 64;
+            uint8_t* dst = smem + L::OFF_KU + j * KUB + lane * 4 * pitch;
+            if (lead) mbar_arrive_expect_tx(full, NH * pitch);
+            __syncwarp();
+            if (lane < 16 && !run)
+              gather4_pair(dst, j < 2 ? &maps.row : &maps.row_pos, 256 * j, r, smem_u32(full));
+            __syncwarp();
+            if (lane < 16 && run && t == 0)
+              load_2d_pair(dst, j < 2 ? &maps.run : &maps.run_pos, 256 * j, r0, smem_u32(full));
+          } else {
+            const uint32_t bar = leader(full);
+            uint8_t* dst = ks + j * KCH * CH + (i * 2 + (t >> 1)) * KCH * 1024 + (t & 1) * 512;
+            if (half == 0 && lead) mbar_arrive_expect_tx(full, 2 * KCH * CH);
+            __syncwarp();
+            if (lane < 16 && !run) {
 #pragma unroll 1
-          for (int i = 0; i < NH / RUN; ++i) {
-            uint8_t* dst = ks + j * KCH * CH + i * 2 * KCH * 1024;
-            if ((run >> i) & 1u) {
-              const int r0 = run_start(r[i * RUN]);
-              if (lead) {
-                load_3d_pair(dst, &maps.run, r0, KCH * j, bar);
-                load_3d_pair(dst + KCH * 1024, &maps.run, r0 + 8, KCH * j, bar);
-              }
-            } else {
-#pragma unroll 1
-              for (int t = 0; t < RUN / 4 * KCH; ++t) {
-                const int c = t >> 2, p = t & 3;
-                const uint4 v = lds16(r + i * RUN + 4 * p);
-                if (lead)
-                  gather4_pair(dst + (p >> 1) * KCH * 1024 + c * 1024 + (p & 1) * 512, &maps.row, 64 * (KCH * j + c), v, bar);
-              }
+              for (int c = 0; c < KCH; ++c) gather4_pair(dst + c * 1024, &maps.row, 64 * (KCH * j + c), r, bar);
             }
             __syncwarp();
-          }
-        }
-        if (lane == 0) mbar_arrive(&r_empty[slot]);
-        __syncwarp();
-        if (u == 0 && ok) ok = load_query(q, seg, lead);   // its keys are on their way
-      }
-    }
-    // the MMAs have read every key, so no load is under way
-#pragma unroll 1
-    for (int j = 0; j < KG && ok && ntile > 0; ++j) ok = await<true>(&k_empty[j], (ntile - 1) & 1, a.err);
-  } else if (!KV8 && warp == 2) {
-    // ------------------------------------------------------------ bf16: values
-    const bool lead = elect_one();
-    bool ok = true;
-    Ring<VR> vr;
-#pragma unroll 1
-    for (int g = 0; g < ntile && ok; ++g) {
-      const uint32_t slot = g % RR;
-      if (!(ok = await<true>(&r_full[slot], (g / RR) & 1, a.err))) break;
-      uint32_t run = runs[slot];
-      const int* r = rows + slot * NT;
-#pragma unroll 1
-      for (int i = 0; i < VS; ++i, r += VT) {
-        if (!(ok = await<true>(&v_empty[vr.slot], vr.use ^ 1, a.err))) break;
-        const uint32_t bar = leader(&v_full[vr.slot]);
-        if (half == 0 && lead) mbar_arrive_expect_tx(&v_full[vr.slot], 2 * VSLOT);
-#pragma unroll 1
-        for (int j = 0; j < VT / RUN; ++j, run >>= 1) {
-          uint8_t* dst = vs + vr.slot * VSLOT + j * VSTEP;
-          if (run & 1u) {
-            const int r0 = run_start(r[j * RUN]);
-            if (lead) load_3d_pair(dst, &maps.run_pos, r0, 4 * half, bar);
-          } else {
-#pragma unroll 1
-            for (int t = 0; t < RUN; ++t) {
-              const int c = t >> 2, p = t & 3;
-              const uint4 v = lds16(r + j * RUN + 4 * p);
-              if (lead) gather4_pair(dst + c * VCH + p * 512, &maps.row, 256 * half + 64 * c, v, bar);
-            }
+            if (lane < 16 && run && (t & 1) == 0) load_3d_pair(dst, &maps.run, r0 < 0 ? r0 : static_cast<int>(r.x), KCH * j, bar);
           }
           __syncwarp();
         }
-        vr.next();
+        if (lane == 0) mbar_arrive(&r_empty[slot]);
+        __syncwarp();
+        if (u == 0 && seg > 0 && ok) ok = load_query(q, seg, lead);   // its keys are on their way
+      }
+    }
+    // the MMAs have read every key, so no load is under way
+    if constexpr (!KV8) {
+#pragma unroll 1
+      for (int j = 0; j < KG && ok && ntile > 0; ++j) ok = await<true>(&k_empty[j], (ntile - 1) & 1, a.err);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ values
+    // A unit is two times 16 rows.  e4m3: lane 4 i + t as above; bf16: lane
+    // 16 i + 4 c + t dims 64 c .. 64 c + 63 of rows 4 t .. 4 t + 3, or lane 16 i
+    // all of a run.
+    const bool lead = elect_one();
+    bool ok = true;
+    Ring<KV8 ? VUR : VR> ur;
+#pragma unroll 1
+    for (int g = 0; g < ntile && ok; ++g) {
+      const uint32_t slot = g % RR;
+      if (!(ok = await<true>(&r_full[slot], (g / RR) & 1, a.err))) break;
+      const int i = KV8 ? lane >> 2 & 1 : lane >> 4;
+      const uint32_t run_bits = runs[slot] >> i;
+      const int* rr = rows + slot * NT + i * RUN + 4 * (lane & 3);
+#pragma unroll 1
+      for (int c = 0; c < VS; ++c, rr += VT) {
+        const uint4 r = lds16(rr);
+        const bool run = (run_bits >> (2 * c)) & 1u;
+        const int r0 = run_start(static_cast<int>(r.x));
+        uint64_t* full = KV8 ? &vu_full[ur.slot] : &v_full[ur.slot];
+        if (!(ok = await<true>(KV8 ? &vu_empty[ur.slot] : &v_empty[ur.slot], ur.use ^ 1, a.err))) break;
+        if constexpr (KV8) {
+          uint8_t* dst = smem + L::OFF_VU + ur.slot * VUB + lane * 1024;
+          if (lead) mbar_arrive_expect_tx(full, VUB);
+          __syncwarp();
+          if (lane < 8 && !run) gather4_pair(dst, &maps.row, 256 * half, r, smem_u32(full));
+          __syncwarp();
+          if (lane < 8 && run && (lane & 3) == 0) load_2d_pair(dst, &maps.run, 256 * half, r0, smem_u32(full));
+        } else {
+          const uint32_t bar = leader(full);
+          const int d = lane >> 2 & 3;
+          uint8_t* dst = vs + ur.slot * VSLOT + i * VSTEP + d * VCH + (lane & 3) * 512;
+          if (half == 0 && lead) mbar_arrive_expect_tx(full, 2 * VSLOT);
+          __syncwarp();
+          if (!run) gather4_pair(dst, &maps.row, 256 * half + 64 * d, r, bar);
+          __syncwarp();
+          if (run && (lane & 15) == 0) load_3d_pair(dst, &maps.run_pos, r0, 4 * half, bar);
+        }
+        __syncwarp();
+        ur.next();
       }
       if (lane == 0) mbar_arrive(&r_empty[slot]);
       __syncwarp();
     }
+    if constexpr (!KV8) {
 #pragma unroll 1
-    for (int i = 0; i < VR && ok && ntile > 0; ++i) {
-      ok = await<true>(&v_empty[vr.slot], vr.use ^ 1, a.err);
-      vr.next();
+      for (int i = 0; i < VR && ok && ntile > 0; ++i) {
+        ok = await<true>(&v_empty[ur.slot], ur.use ^ 1, a.err);
+        ur.next();
+      }
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ row look-up
@@ -741,11 +721,12 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     // each step of the loop issues one for each of three tiles.
     bool ok = true, bad = false;
     int q = q0 - 1, off = 0, n = 0, left = ntile, u = 0;
-    int b = 0, vis = 0;
+    int vis = 0;
     List ls = {};
     int pos[4], at[4], pg[4], row[4];                // tile i; tile i - 1; tile i - 2
     float s[4];
-    int b1 = 0, vis1 = 0;
+    const int32_t *pages = a.page_table, *pages1 = pages;
+    int vis1 = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) pos[k] = at[k] = pg[k] = row[k] = -1;
 #pragma unroll 1
@@ -817,7 +798,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       for (int k = 0; k < 4; ++k) {
         at[k] = pos[k] >= 0 && pos[k] < vis1 ? pos[k] : -1;
         bad |= at[k] != pos[k] && pos[k] != -1;
-        pg[k] = at[k] >= 0 ? __ldg(a.page_table + static_cast<size_t>(b1) * a.max_pages + (at[k] >> a.page_shift)) : -1;
+        pg[k] = at[k] >= 0 ? __ldg(pages1 + (at[k] >> a.page_shift)) : -1;
       }
       if (i < ntile && u == n) {
         ++q;
@@ -825,7 +806,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         n = min(tiles_of<IDX>(a, q) - off, left);
         left -= n;
         u = 0;
-        b = seq_of_query(a.q_offsets, a.B, q, lane);
+        pages = a.page_table + static_cast<size_t>(seq_of_query(a.q_offsets, a.B, q, lane)) * a.max_pages;
         vis = visible(a, q);
         bad |= __ldg(a.q_vis + q) > vis;
         ls = list_of(a, vis);
@@ -842,7 +823,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
           }
         }
       }
-      b1 = b;
+      pages1 = pages;
       vis1 = vis;
       ++u;
     }
@@ -969,7 +950,11 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       if (!whole) (head ? head_q : tail_q) = q;
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // NaN stays NaN
       const bool none = l == 0.f;
+      // A part goes out as [dim / 4][head][4 dims], so that the lanes of a warp
+      // write next to one another; a result by way of this warp's eighth of P,
+      // 64 bytes of eight heads a store.
       const int d0 = 256 * hh + 128 * cg;
+      uint8_t* stage = ps + (warp - SMX0) * 2048;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         float o[32];
@@ -978,15 +963,26 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] = none ? 0.f : o[i] * inv;
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + (static_cast<size_t>(q) * a.H + h) * DSA_DIM_V + d0 + 32 * c);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            dst[i] = make_uint4(bf16x2_bits(o[8 * i], o[8 * i + 1]), bf16x2_bits(o[8 * i + 2], o[8 * i + 3]),
-                                bf16x2_bits(o[8 * i + 4], o[8 * i + 5]), bf16x2_bits(o[8 * i + 6], o[8 * i + 7]));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(a.o_part + (static_cast<size_t>(part) * a.H + h) * DSA_DIM_V + d0 + 32 * c);
+            *reinterpret_cast<uint4*>(stage + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)) =
+                make_uint4(bf16x2_bits(o[8 * i], o[8 * i + 1]), bf16x2_bits(o[8 * i + 2], o[8 * i + 3]),
+                           bf16x2_bits(o[8 * i + 4], o[8 * i + 5]), bf16x2_bits(o[8 * i + 6], o[8 * i + 7]));
+          __syncwarp();
+          const int piece = lane & 3;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 4; ++i) {
+            const int hr = 8 * i + (lane >> 2);
+            const uint4 w = lds16(stage + hr * 64 + ((piece ^ (hr >> 1 & 3)) << 4));
+            const size_t row = static_cast<size_t>(q) * a.H + half * HC + (quarter & 1) * 32 + hr;
+            *reinterpret_cast<uint4*>(a.out + row * DSA_DIM_V + d0 + 32 * c + 8 * piece) = w;
+          }
+          __syncwarp();
+        } else {
+          float4* dst = reinterpret_cast<float4*>(a.o_part) +
+                        (static_cast<size_t>(part) * (DSA_DIM_V / 4) + (d0 + 32 * c) / 4) * a.H + h;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i * a.H] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
       if (hh == 0 && cg == 0)
@@ -999,146 +995,109 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       a.desc[2 * pair + 1] = head_q;
     }
     __syncwarp();
-  } else if (KV8 && warp < SMX0 + SMX + GROUP) {
-    // ------------------------------------------------------------ e4m3: keys widened, queries scaled
-    // Two chunks at a time.  thread: 16 codes of four tokens; the lanes of the
-    // upper chunk store their two pieces in the other order, so that the eight
+  } else if (KV8) {
+    // ------------------------------------------------------------ e4m3: codes widened, queries scaled
+    // In the order of the MMAs: the keys of a tile, two chunks at a time, then
+    // the values of the tile before.  thread: 16 codes of two tokens.  Lanes of
+    // odd chunks store their two pieces in the other order, so that the eight
     // lanes of a store lie in different banks.
     const int lw = warp - (SMX0 + SMX);
     const int lt = lw * 32 + lane;
-    const int pc = lt & 7, r0 = lt >> 3, flip = pc >> 2;
-    const int pp = lt & 3, rp = lt >> 2;             // the positions: 16 codes of two tokens
     bool ok = true;
-    int q = q0, off = off0, left = ntile;
-    uint32_t g = 0;
+    int q = q0, off = off0, left = ntile, n = 0, u = 0;
+    uint32_t seg = 0;
+    Ring<VR> vr;
+    Ring<VUR> ur;
 
-    // The query as fp16 in place, each head scaled so that its largest element
-    // lies in [2^14, 2^15); infinities and NaN stay what they are.  A warp takes
-    // a quarter of the heads, two at a time; 72 pieces of 8 dims a head.
-    auto query = [&](uint32_t seg) {
+    auto query = [&]() {
       if (!(ok = ok && await(q_raw, seg & 1, a.err))) return;
-#pragma unroll 1
-      for (int h0 = (HC >> 2) * lw; h0 < (HC >> 2) * (lw + 1); h0 += 2) {
-        uint4 v[2][3];
-        auto piece = [&](int r, int k) {
-          const int p = 32 * k + lane;
-          return reinterpret_cast<uint4*>(qs + (p >> 3) * CH + r * 128 + (((p & 7) ^ (r & 7)) << 4));
-        };
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int k = 0; k < 3; ++k) v[i][k] = k < 2 || lane < 8 ? *piece(h0 + i, k) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int k = 0; k < 3; ++k) m = mag2(mag2(mag2(mag2(m, v[i][k].x), v[i][k].y), v[i][k].z), v[i][k].w);
-          m = max(m & 0xFFFFu, m >> 16);
-          m = __reduce_max_sync(0xffffffffu, m);
-          const int e = min(max(static_cast<int>(m >> 7), 14), 254);
-          const float s = m == 0 || m >= 0x7F80u ? 1.f : __uint_as_float(static_cast<uint32_t>(min(254, 268 - e)) << 23);
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
-            if (k < 2 || lane < 8)
-              *piece(h0 + i, k) = make_uint4(scale_pair(v[i][k].x, s), scale_pair(v[i][k].y, s),
-                                             scale_pair(v[i][k].z, s), scale_pair(v[i][k].w, s));
-          if (lane == 0) qmul[(seg & 1) * RH + h0 + i] = __fdiv_rn(1.f, s);
-        }
-      }
+      scale_query(qs, qmul + (seg & 1) * RH, HC >> 3, lw, lane);
       hand_over(q_full);
-      __syncwarp();
     };
 
 #pragma unroll 1
-    for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
-      const int n = min(tiles_of<IDX>(a, q) - off, left);
-      left -= n;
+    for (int g = 0; g <= ntile && ok; ++g) {
+      const bool first = u == n;                     // tile g is a segment's first
+      if (first && g < ntile) {
+        if (g > 0) {
+          ++q;
+          ++seg;
+          off = 0;
+        }
+        n = min(tiles_of<IDX>(a, q) - off, left);
+        left -= n;
+        u = 0;
+      }
+      // the MMAs finish a segment's values before the next one's scores
 #pragma unroll 1
-      for (int u = 0; u < n && ok; ++u, ++g) {
-        const uint32_t slot = g % RR;
-        if (!(ok = await(&r_full[slot], (g / RR) & 1, a.err))) break;
-        const __half2* fs = fold + slot * NT + half * NH;
-        __half2 f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) f[i] = fs[r0 + 16 * i];
+      for (int turn = 0; turn < 2 && ok; ++turn) {
+        if ((turn == 0) != first) {
+          if (g == ntile) continue;
+          const uint32_t slot = g % RR;
+          // the first query while its rows are looked up, others when the slots of
+          // their keys are full
+          if (g == 0) query();
+          if (!(ok = ok && await(&r_full[slot], (g / RR) & 1, a.err))) break;
+          const __half2* fs = fold + slot * NT + half * NH;
+          const int pc = lt & 7, r0 = lt >> 3, flip = pc >> 2;
+          const __half2 f0 = fs[r0], f1 = fs[r0 + 32];
 #pragma unroll 1
-        for (int d = 0; d < 4; ++d) {
-          if (u == 0 && d == 2) query(seg);          // both slots are full: their scores wait for the query
-          if ((d & 1) == 0) ok = ok && await(&ku_full[d >> 1], g & 1, a.err);
-          const uint8_t* src = smem + L::OFF_KU + (d >> 1) * KUB + (d & 1) * 128 + pc * 16;
-          uint4 v[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = lds16(src + (r0 + 16 * i) * 256);
-          if (!(ok = ok && await(&k_empty[d & 1], key_use(d, g) ^ 1, a.err))) break;
-          uint8_t* dst = ks + (2 * (d & 1) + flip) * CH + r0 * 128;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) store_wide(dst + i * 16 * 128, 2 * (pc & 3), r0 & 7, flip, v[i], f[i]);
-          hand_over(&k_full[d & 1]);
-          if ((d & 1) && lane == 0) mbar_arrive(&ku_empty[d >> 1]);   // only now: the stores have waited for the loads
+          for (int d = 0; d < 4; ++d) {
+            if (first && g > 0 && d == 2) query();
+            if ((d & 1) == 0) ok = ok && await(&ku_full[d >> 1], g & 1, a.err);
+            const uint8_t* src = smem + L::OFF_KU + (d >> 1) * KUB + (d & 1) * 128 + r0 * 256 + pc * 16;
+            const uint4 v0 = lds16(src), v1 = lds16(src + 32 * 256);
+            if (!(ok = ok && await(&k_empty[d & 1], key_use(d, g) ^ 1, a.err))) break;
+            uint8_t* dst = ks + (2 * (d & 1) + flip) * CH + r0 * 128;
+            store_wide(dst, 2 * (pc & 3), r0 & 7, flip, v0, f0);
+            store_wide(dst + 32 * 128, 2 * (pc & 3), r0 & 7, flip, v1, f1);
+            hand_over(&k_full[d & 1]);
+            if ((d & 1) && lane == 0) mbar_arrive(&ku_empty[d >> 1]);   // only now: the stores have waited for the loads
+            __syncwarp();
+          }
+          ok = ok && await(&ku_full[2], g & 1, a.err);
+          const int rp = lt >> 2;
+          const uint4 v = lds16(smem + L::OFF_KU + 2 * KUB + lt * 16);
+          if (!(ok = ok && await(&k_empty[2], (g & 1) ^ 1, a.err))) break;
+          store_wide(ks + 4 * CH + rp * 128, 2 * (lt & 3), rp & 7, 0, v, fs[rp]);
+          hand_over(&k_full[2]);
+          if (lane == 0) mbar_arrive(&ku_empty[2]);
+          __syncwarp();
+          ++u;
+        } else if (g > 0) {
+          const uint32_t slot = (g - 1) % RR;
+          const int pc = lt & 15, r0 = lt >> 4, flip = pc >> 2 & 1;
+          const __half2* fs = fold + slot * NT + r0;
+#pragma unroll 1
+          for (int c = 0; c < VS; ++c, fs += VT) {
+            ok = ok && await(&vu_full[ur.slot], ur.use, a.err);
+            const uint8_t* src = smem + L::OFF_VU + ur.slot * VUB + lt * 16;
+            const uint4 v0 = lds16(src), v1 = lds16(src + 16 * 256);
+            const __half2 f0 = fs[0], f1 = fs[16];
+            if (!(ok = ok && await(&v_empty[vr.slot], vr.use ^ 1, a.err))) break;
+            uint8_t* dst = vs + vr.slot * VSLOT + (pc >> 2) * VCH + r0 * 128;
+            store_wide(dst, 2 * (pc & 3), r0 & 7, flip, v0, f0);
+            store_wide(dst + VSTEP, 2 * (pc & 3), r0 & 7, flip, v1, f1);
+            hand_over(&v_full[vr.slot]);
+            if (lane == 0) mbar_arrive(&vu_empty[ur.slot]);
+            __syncwarp();
+            vr.next();
+            ur.next();
+          }
+          if (lane == 0) mbar_arrive(&r_empty[slot]);
           __syncwarp();
         }
-        ok = ok && await(&ku_full[2], g & 1, a.err);
-        uint4 v[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) v[i] = lds16(smem + L::OFF_KU + 2 * KUB + (rp + 32 * i) * 64 + pp * 16);
-        if (!(ok = ok && await(&k_empty[2], (g & 1) ^ 1, a.err))) break;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) store_wide(ks + 4 * CH + (rp + 32 * i) * 128, 2 * pp, rp & 7, 0, v[i], fs[rp + 32 * i]);
-        hand_over(&k_full[2]);
-        if (lane == 0) mbar_arrive(&ku_empty[2]);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&r_empty[slot]);
-        __syncwarp();
       }
     }
-    // the MMAs have read every key
-    if (ok && ntile > 0)
+    // the MMAs have read every key and value
+    if (ok && ntile > 0) {
       ok = await<true>(&k_empty[0], 1, a.err) && await<true>(&k_empty[1], 1, a.err) &&
            await<true>(&k_empty[2], (ntile - 1) & 1, a.err);
-  } else if (KV8) {
-    // ------------------------------------------------------------ e4m3: values widened
-    // A unit at a time.  thread: 16 codes of four tokens; lanes of odd chunks
-    // store their two pieces in the other order, as above.
-    const int lt = (warp - (SMX0 + SMX + GROUP)) * 32 + lane;
-    const int pc = lt & 15, r0 = lt >> 4, flip = (pc >> 2) & 1;
-    bool ok = true;
-    Ring<VR> vr;
-    Ring<VUR> ur;
 #pragma unroll 1
-    for (int g = 0; g < ntile && ok; ++g) {
-      const uint32_t slot = g % RR;
-      if (!(ok = await(&r_full[slot], (g / RR) & 1, a.err))) break;
-      const __half2* fs = fold + slot * NT + r0;
-#pragma unroll 1
-      for (int c = 0; c < VS; ++c, fs += VT) {
-        ok = await(&vu_full[ur.slot], ur.use, a.err);
-        const uint8_t* src = smem + L::OFF_VU + ur.slot * VUB + r0 * 256 + pc * 16;
-        uint4 v[4];
-        __half2 f[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = lds16(src + i * 8 * 256);
-          f[i] = fs[8 * i];
-        }
-        if (!(ok = ok && await(&v_empty[vr.slot], vr.use ^ 1, a.err))) break;
-        uint8_t* dst = vs + vr.slot * VSLOT + (pc >> 2) * VCH + r0 * 128;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          store_wide(dst + (i >> 1) * VSTEP + (i & 1) * 1024, 2 * (pc & 3), r0 & 7, flip, v[i], f[i]);
-        hand_over(&v_full[vr.slot]);
-        if (lane == 0) mbar_arrive(&vu_empty[ur.slot]);
-        __syncwarp();
+      for (int i = 0; i < VR && ok; ++i) {
+        ok = await<true>(&v_empty[vr.slot], vr.use ^ 1, a.err);
         vr.next();
-        ur.next();
       }
-      if (lane == 0) mbar_arrive(&r_empty[slot]);
-      __syncwarp();
-    }
-    // the MMAs have read every value
-#pragma unroll 1
-    for (int i = 0; i < VR && ok && ntile > 0; ++i) {
-      ok = await<true>(&v_empty[vr.slot], vr.use ^ 1, a.err);
-      vr.next();
     }
   }
 
@@ -1156,39 +1115,50 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
 // the first part of query desc[2p + 1] in part 2p + 1, the pairs after it the
 // others in parts 2(p + i), where desc[2(p + i)] is that query again.
 //   LSE = ln sum_i exp(LSE_i),  O = sum_i exp(LSE_i - LSE) O_i.
-// grid (pairs, H / 4): 4 heads a CTA, a float4 of one head's output a thread.
-constexpr int MT = 512;
+// The parts lie as [dim / 4][head][4 dims].  grid (pairs, H / 32, 8): 32 heads,
+// a lane each, and 64 dims a CTA, 8 a warp; the result turns in shared memory.
+constexpr int MT = 256;
 __global__ void __launch_bounds__(MT) attend_merge_kernel(const int32_t* desc, const float* o_part,
                                                           const float* l_part, int H, __nv_bfloat16* out,
                                                           float* lse) {
+  __shared__ uint4 turn[32][9];
   pdl_wait();
   const int p = blockIdx.x, pairs = gridDim.x;
   const int q = desc[2 * p + 1];
   if (q < 0) return;
   int n = 1;
   while (p + n < pairs && desc[2 * (p + n)] == q) ++n;
-  const int h = blockIdx.y * 4 + (threadIdx.x >> 7), c = threadIdx.x & 127;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int h = blockIdx.y * 32 + lane, d4 = blockIdx.z * 16 + 2 * warp;
   float m = -INFINITY;
   for (int i = 0; i < n; ++i) m = fmaxf(m, l_part[static_cast<size_t>(2 * (p + i) + (i == 0)) * H + h]);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float acc[8] = {};
   float tot = 0.f;
   const float m_eff = m == -INFINITY ? 0.f : m;
 #pragma unroll 4
   for (int i = 0; i < n; ++i) {
-    const size_t at = static_cast<size_t>(2 * (p + i) + (i == 0)) * H + h;
-    const float w = expf(l_part[at] - m_eff);
-    const float4 v = reinterpret_cast<const float4*>(o_part + at * DSA_DIM_V)[c];
+    const size_t part = 2 * (p + i) + (i == 0);
+    const float w = expf(l_part[part * H + h] - m_eff);
+    const float4* src = reinterpret_cast<const float4*>(o_part) + (part * (DSA_DIM_V / 4) + d4) * H + h;
+    const float4 a = src[0], b = src[H];
     tot += w;
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
+    acc[0] = fmaf(w, a.x, acc[0]);
+    acc[1] = fmaf(w, a.y, acc[1]);
+    acc[2] = fmaf(w, a.z, acc[2]);
+    acc[3] = fmaf(w, a.w, acc[3]);
+    acc[4] = fmaf(w, b.x, acc[4]);
+    acc[5] = fmaf(w, b.y, acc[5]);
+    acc[6] = fmaf(w, b.z, acc[6]);
+    acc[7] = fmaf(w, b.w, acc[7]);
   }
   const float inv = tot == 0.f ? 0.f : 1.f / tot;
-  const size_t qh = static_cast<size_t>(q) * H + h;
-  reinterpret_cast<uint2*>(out + qh * DSA_DIM_V)[c] =
-      make_uint2(bf16x2_bits(acc.x * inv, acc.y * inv), bf16x2_bits(acc.z * inv, acc.w * inv));
-  if (c == 0) lse[qh] = tot == 0.f ? -INFINITY : m_eff + logf(tot);
+  turn[lane][warp] = make_uint4(bf16x2_bits(acc[0] * inv, acc[1] * inv), bf16x2_bits(acc[2] * inv, acc[3] * inv),
+                                bf16x2_bits(acc[4] * inv, acc[5] * inv), bf16x2_bits(acc[6] * inv, acc[7] * inv));
+  if (blockIdx.z == 0 && warp == 0) lse[static_cast<size_t>(q) * H + h] = tot == 0.f ? -INFINITY : m_eff + logf(tot);
+  __syncthreads();
+  const int r = threadIdx.x >> 3, c = threadIdx.x & 7;
+  reinterpret_cast<uint4*>(out + (static_cast<size_t>(q) * H + blockIdx.y * 32 + r) * DSA_DIM_V + 64 * blockIdx.z)[c] =
+      turn[r][c];
 }
 
 constexpr int MAX_PAIRS = 74;
@@ -1280,7 +1250,7 @@ cudaError_t launch_attend(const __nv_bfloat16* q, const void* pool, const float*
                       : (kv_scales ? launch<true, false>(a, m, pairs, st) : launch<false, false>(a, m, pairs, st));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(H / 4), 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(H / 32), DSA_DIM_V / 64);
   cfg.blockDim = dim3(MT, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
