@@ -79,12 +79,12 @@ constexpr int VUR = 2;                               // units of their ring
 constexpr int RUN = 16;                              // rows that one load can bring where they are consecutive
 constexpr int RR = 3;                                // tiles looked up ahead
 constexpr int SMX = 8;                               // softmax warps
-constexpr int CONV = 8;                               // warps that widen codes
+constexpr int GROUP = 4;                             // warps that widen keys; as many widen values
 constexpr int SMX0 = 4;                              // first of the softmax warps
 
 template <bool KV8>
 struct Plan {
-  static constexpr int WARPS = SMX0 + SMX + (KV8 ? CONV : 0);
+  static constexpr int WARPS = SMX0 + SMX + (KV8 ? 2 * GROUP : 0);
   static constexpr int THREADS = 32 * WARPS;
   // A tile's 9 key chunks come in groups, each with its slot: three of three, or
   // (e4m3) four of two, through two slots, and the positions.
@@ -98,9 +98,8 @@ struct Plan {
   static constexpr int OFF_P = OFF_V + VR * VSLOT;   // [2][64 heads x 64 tokens]
   static constexpr int OFF_KU = OFF_P + 2 * CH;      // e4m3: units of a tile's keys
   static constexpr int OFF_VU = OFF_KU + (KV8 ? 2 * KUB + NH * 64 : 0);
-  static constexpr int OFF_SCL = OFF_VU + (KV8 ? VUR * VUB : 0);       // e4m3: float [RR][128]: scale of each token
-  static constexpr int OFF_FOLD = OFF_SCL + (KV8 ? RR * NT * 4 : 0);   // half2 [RR][128]: factor of its codes
-  static constexpr int OFF_TILE = OFF_FOLD + (KV8 ? RR * NT * 4 : 0);  // float4 [RR]: scale, log2, 1 / scale of the tile; w: it has one
+  static constexpr int OFF_SCL = OFF_VU + (KV8 ? VUR * VUB : 0);       // e4m3: float [RR][128]: scale of each token, over the tile's where it has one
+  static constexpr int OFF_TILE = OFF_SCL + (KV8 ? RR * NT * 4 : 0);  // float4 [RR]: scale, log2, 1 / scale of the tile; w: it has one
   static constexpr int OFF_ROWS = OFF_TILE + (KV8 ? RR * 16 : 0);      // int32 [RR][128]: pool row or -1
   static constexpr int OFF_MASK = OFF_ROWS + RR * NT * 4;            // uint32 [RR][4]: tokens that count
   static constexpr int OFF_RUNS = OFF_MASK + RR * 4 * 4;             // uint32 [4]: bit i: rows 16 i .. 16 i + 15 are consecutive, or none is held
@@ -197,16 +196,25 @@ __device__ __forceinline__ int seq_of_query(const int32_t* q_offsets, int B, int
   return lo;
 }
 
-// Waits of a whole warp for the phase of the given parity, polled and bounded
-// by their number of tries (a try takes about 100 cycles, so they end after
-// about two seconds).  One compact loop: the code of all roles together has to
-// stay in the instruction cache, see below.  NAP: where a late answer costs nothing.
-constexpr uint32_t WAIT_TRIES = 1u << 25;
-template <bool NAP = false>
+// Waits of a whole warp for the phase of the given parity, bounded by their
+// number of tries (about two seconds).  A try suspends the warp for up to
+// WAIT_NS, so that it leaves the issue slots to others: polled barriers took half of
+// all slots.  The limit bounds how late an arrival from the peer CTA is seen.
+constexpr uint32_t WAIT_TRIES = 1u << 22, WAIT_NS = 200;
+__device__ __forceinline__ bool try_wait_ns(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(WAIT_NS)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, uint32_t* err) {
 #pragma unroll 1
-  for (uint32_t it = 0; !__all_sync(0xffffffffu, mbar_test_wait(bar, parity)); ++it) {
-    if constexpr (NAP) __nanosleep(20);
+  for (uint32_t it = 0; !__all_sync(0xffffffffu, try_wait_ns(bar, parity)); ++it) {
     if (it == WAIT_TRIES) {
       raise_error(err, DEVERR_TIMEOUT);
       return false;
@@ -298,9 +306,9 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// four e4m3 codes -> four fp16 times f (a power of two), exactly.  Written in
-// PTX: the intrinsic of the pair type costs twice the instructions.
-__device__ __forceinline__ uint2 widen4(uint32_t w, __half2 f) {
+// four e4m3 codes -> four fp16, exactly.  Written in PTX: the intrinsic of the
+// pair type costs twice the instructions.
+__device__ __forceinline__ uint2 widen4(uint32_t w) {
   uint2 r;
   asm("{\n\t.reg .b16 lo, hi;\n\t"
       "mov.b32 {lo, hi}, %2;\n\t"
@@ -308,9 +316,7 @@ __device__ __forceinline__ uint2 widen4(uint32_t w, __half2 f) {
       "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
       : "=r"(r.x), "=r"(r.y)
       : "r"(w));
-  const __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&r.x), f);
-  const __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&r.y), f);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  return r;
 }
 
 // one lane of a converged warp
@@ -335,16 +341,16 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t w, float s) {
 
 // 16 codes of a token, widened: pieces p and p + 1 of the 128-byte row dst, whose
 // swizzle is sw; `flip` stores the second first
-__device__ __forceinline__ void store_wide(uint8_t* dst, int p, int sw, int flip, uint4 c, __half2 f) {
-  const uint2 w0 = widen4(c.x, f), w1 = widen4(c.y, f), w2 = widen4(c.z, f), w3 = widen4(c.w, f);
+__device__ __forceinline__ void store_wide(uint8_t* dst, int p, int sw, int flip, uint4 c) {
+  const uint2 w0 = widen4(c.x), w1 = widen4(c.y), w2 = widen4(c.z), w3 = widen4(c.w);
   const uint4 lo = make_uint4(w0.x, w0.y, w1.x, w1.y), hi = make_uint4(w2.x, w2.y, w3.x, w3.y);
   *reinterpret_cast<uint4*>(dst + (((p + flip) ^ sw) << 4)) = flip ? hi : lo;
   *reinterpret_cast<uint4*>(dst + (((p + 1 - flip) ^ sw) << 4)) = flip ? lo : hi;
 }
 
 // The query as fp16 in place, each head scaled so that its largest element lies
-// in [2^14, 2^15); infinities and NaN stay what they are.  A warp takes an
-// eighth of the heads, two at a time; 72 pieces of 8 dims a head.  A function of
+// in [2^14, 2^15); infinities and NaN stay what they are.  A warp takes a
+// quarter of the heads, two at a time; 72 pieces of 8 dims a head.  A function of
 // its own, since two places call it.
 __device__ __noinline__ void scale_query(uint8_t* qs, float* qmul, int heads, int lw, int lane) {
 #pragma unroll 1
@@ -376,6 +382,8 @@ __device__ __noinline__ void scale_query(uint8_t* qs, float* qmul, int heads, in
   }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // first row of a run: of rows that the list does not hold, all before the pool
 __device__ __forceinline__ int run_start(int row) { return row < 0 ? -RUN : row; }
 
@@ -390,7 +398,6 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   uint8_t* vs = smem + L::OFF_V;
   uint8_t* ps = smem + L::OFF_P;
   float* scl = reinterpret_cast<float*>(smem + L::OFF_SCL);
-  __half2* fold = reinterpret_cast<__half2*>(smem + L::OFF_FOLD);
   float4* tsc = reinterpret_cast<float4*>(smem + L::OFF_TILE);
   int* rows = reinterpret_cast<int*>(smem + L::OFF_ROWS);
   uint32_t* mask = reinterpret_cast<uint32_t*>(smem + L::OFF_MASK);
@@ -437,14 +444,14 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   if (tid < L::NBAR) {
     // arrivals a phase: one, but for these
     const int i = tid;
-    const int full = KV8 ? 2 * CONV : 1;             // widened operands: a warp each
+    const int full = KV8 ? 2 * GROUP : 1;            // widened operands: a warp each
     int n = 1;
-    if (i >= RR && i < 2 * RR) n = 2 + live_smx + (KV8 ? CONV : 0);
+    if (i >= RR && i < 2 * RR) n = 2 + live_smx;
     if (i >= k_full - bars && i < k_empty - bars) n = full;
     if (i >= v_full - bars && i < v_empty - bars) n = full;
     if (i == p_full - bars) n = 2 * live_smx;
     if (i == q_full - bars) n = full;
-    if (KV8 && ((i >= ku_empty - bars && i < vu_full - bars) || i >= vu_empty - bars)) n = CONV;
+    if (KV8 && ((i >= ku_empty - bars && i < vu_full - bars) || i >= vu_empty - bars)) n = GROUP;
     mbar_init(bars + i, n);
     mbar_fence_init();
   }
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   auto key_use = [](int j, uint32_t g) { return KV8 && j < 4 ? static_cast<uint32_t>(j >> 1) : g & 1; };
   // the query of a segment, once the scores of the one before are done
   auto load_query = [&](int q, uint32_t seg, bool lead) {
-    if (seg > 0 && !await<true>(q_empty, (seg - 1) & 1, a.err)) return false;
+    if (seg > 0 && !await(q_empty, (seg - 1) & 1, a.err)) return false;
     if (lead) {
       const uint32_t bytes = static_cast<uint32_t>(KC * 128 * HC);
       const uint32_t bar = KV8 ? smem_u32(q_raw) : leader(q_full);
@@ -620,15 +627,16 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
 #pragma unroll 1
       for (int u = 0; u < n && ok; ++u, ++g) {
         const uint32_t slot = g % RR;
-        if (!(ok = await<true>(&r_full[slot], (g / RR) & 1, a.err))) break;
-        const bool run = (runs[slot] >> (half * (NH / RUN) + (lane >> 2 & 3))) & 1u;
+        if (!(ok = await(&r_full[slot], (g / RR) & 1, a.err))) break;
+        const bool run = KV8 ? runs[slot] >> (half * (NH / 16) + (lane >> 2 & 3)) & 1u
+                             : runs[slot] >> (8 + half * (NH / 8) + (lane >> 1 & 7)) & 1u;
         const uint4 r = lds16(rows + slot * NT + half * NH + 4 * (lane & 15));
         const int r0 = run_start(static_cast<int>(r.x));
         const int i = lane >> 2, t = lane & 3;
 #pragma unroll 1
         for (int j = 0; j < 3; ++j) {
           uint64_t* full = KV8 ? &ku_full[j] : &k_full[j];
-          if (!(ok = await<true>(KV8 ? &ku_empty[j] : &k_empty[j], (g & 1) ^ 1, a.err))) break;
+          if (!(ok = await(KV8 ? &ku_empty[j] : &k_empty[j], (g & 1) ^ 1, a.err))) break;
           if constexpr (KV8) {
             const int pitch = j < 2 ? 256 : 64;
             uint8_t* dst = smem + L::OFF_KU + j * KUB + lane * 4 * pitch;
@@ -661,7 +669,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     // the MMAs have read every key, so no load is under way
     if constexpr (!KV8) {
 #pragma unroll 1
-      for (int j = 0; j < KG && ok && ntile > 0; ++j) ok = await<true>(&k_empty[j], (ntile - 1) & 1, a.err);
+      for (int j = 0; j < KG && ok && ntile > 0; ++j) ok = await(&k_empty[j], (ntile - 1) & 1, a.err);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------ values
@@ -674,7 +682,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
 #pragma unroll 1
     for (int g = 0; g < ntile && ok; ++g) {
       const uint32_t slot = g % RR;
-      if (!(ok = await<true>(&r_full[slot], (g / RR) & 1, a.err))) break;
+      if (!(ok = await(&r_full[slot], (g / RR) & 1, a.err))) break;
       const int i = KV8 ? lane >> 2 & 1 : lane >> 4;
       const uint32_t run_bits = runs[slot] >> i;
       const int* rr = rows + slot * NT + i * RUN + 4 * (lane & 3);
@@ -684,7 +692,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         const bool run = (run_bits >> (2 * c)) & 1u;
         const int r0 = run_start(static_cast<int>(r.x));
         uint64_t* full = KV8 ? &vu_full[ur.slot] : &v_full[ur.slot];
-        if (!(ok = await<true>(KV8 ? &vu_empty[ur.slot] : &v_empty[ur.slot], ur.use ^ 1, a.err))) break;
+        if (!(ok = await(KV8 ? &vu_empty[ur.slot] : &v_empty[ur.slot], ur.use ^ 1, a.err))) break;
         if constexpr (KV8) {
           uint8_t* dst = smem + L::OFF_VU + ur.slot * VUB + lane * 1024;
           if (lead) mbar_arrive_expect_tx(full, VUB);
@@ -711,7 +719,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     if constexpr (!KV8) {
 #pragma unroll 1
       for (int i = 0; i < VR && ok && ntile > 0; ++i) {
-        ok = await<true>(&v_empty[ur.slot], ur.use ^ 1, a.err);
+        ok = await(&v_empty[ur.slot], ur.use ^ 1, a.err);
         ur.next();
       }
     }
@@ -734,13 +742,12 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       if (i >= 3) {
         // tile i - 3: hand it over
         const uint32_t g = i - 3, slot = g % RR;
-        if (!(ok = await<true>(&r_empty[slot], ((g / RR) & 1) ^ 1, a.err))) break;
+        if (!(ok = await(&r_empty[slot], ((g / RR) & 1) ^ 1, a.err))) break;
         if constexpr (KV8) {
-          // Scales that differ by powers of two, up to 2^15, go into the fp16
-          // codes, exactly (a code is a multiple of 2^-9, fp16's least step is
-          // 2^-24): the tile then has one scale, its largest.  Other tiles keep
-          // one a token.
-          uint32_t lo = 0xffffffffu, hi = 0, mlo = 0xffffffffu, mhi = 0;
+          // A tile has one scale, its largest, where the others are at least
+          // 2^-15 of it, so that P times their ratio stays within fp16; other tiles
+          // keep one a token.
+          uint32_t lo = 0xffffffffu, hi = 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (row[k] >= 0 && !(s[k] >= 0x1p-40f && s[k] <= 0x1p40f)) {
@@ -748,26 +755,18 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
               bad = true;
             }
             if (row[k] >= 0) {
-              const uint32_t bits = __float_as_uint(s[k]);
-              lo = min(lo, bits);
-              hi = max(hi, bits);
-              mlo = min(mlo, bits & 0x7FFFFFu);
-              mhi = max(mhi, bits & 0x7FFFFFu);
+              lo = min(lo, __float_as_uint(s[k]));
+              hi = max(hi, __float_as_uint(s[k]));
             }
           }
           lo = __reduce_min_sync(0xffffffffu, lo);
           hi = __reduce_max_sync(0xffffffffu, hi);
-          mlo = __reduce_min_sync(0xffffffffu, mlo);
-          mhi = __reduce_max_sync(0xffffffffu, mhi);
-          const bool one = hi == 0 || (mlo == mhi && (hi - lo) >> 23 <= 15);
           const float st = hi == 0 ? 1.f : __uint_as_float(hi), inv = __fdiv_rn(1.f, st);
+          const bool one = hi == 0 || __uint_as_float(lo) >= st * 0x1p-15f;
           if (lane == 0) tsc[slot] = make_float4(st * a.scale_log2, log2f(st), inv, one ? 1.f : 0.f);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (row[k] < 0) s[k] = st;
-            scl[slot * NT + 32 * k + lane] = s[k];
-            fold[slot * NT + 32 * k + lane] = __float2half2_rn(one ? s[k] * inv : 1.f);
-          }
+          for (int k = 0; k < 4; ++k)
+            scl[slot * NT + 32 * k + lane] = row[k] < 0 ? 1.f : one ? s[k] * inv : s[k];
         }
         uint32_t run = 0;
 #pragma unroll
@@ -779,6 +778,13 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
           const uint32_t c =
               __ballot_sync(0xffffffffu, first >= 0 ? row[k] == first + (lane & 15) : row[k] < 0);
           run |= ((c & 0xFFFFu) == 0xFFFFu ? 1u : 0u) << (2 * k) | (c >> 16 == 0xFFFFu ? 2u : 0u) << (2 * k);
+          if constexpr (!KV8) {
+            // bf16 keys: runs of 8 rows, in the upper bits
+            const int first8 = __shfl_sync(0xffffffffu, row[k], lane & 24);
+            const uint32_t c8 = __ballot_sync(0xffffffffu, first8 >= 0 ? row[k] == first8 + (lane & 7) : row[k] < 0);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) run |= ((c8 >> (8 * b) & 0xFFu) == 0xFFu ? 1u : 0u) << (8 + 4 * k + b);
+          }
         }
         if (lane == 0) runs[slot] = run;
         __syncwarp();
@@ -793,6 +799,14 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         if (pg[k] >= 0 && pg[k] < a.num_pages) row[k] = (pg[k] << a.page_shift) + (at[k] & ((1 << a.page_shift) - 1));
         bad |= at[k] >= 0 && row[k] < 0;
         if constexpr (KV8) s[k] = row[k] >= 0 ? __ldg(a.kv_scales + (row[k] >> a.block_shift)) : 1.f;
+        // The row on its way to L2, half a row a CTA: it is loaded about two tiles
+        // from now, which a load from DRAM would not quite fit into.
+        if (row[k] >= 0) {
+          constexpr int ROW = DSA_DIM * (KV8 ? 1 : 2), LINES = (ROW / 2 + 127) / 128;
+          const uint8_t* at_row = a.pool + static_cast<size_t>(row[k]) * ROW + half * (ROW / 2);
+#pragma unroll
+          for (int l = 0; l < LINES; ++l) prefetch_l2(at_row + l * 128);
+        }
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -867,8 +881,19 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         const float* sc = scl + slot * NT + hh * NH + cg * 32;
         if (one) {
           const float k = ts.x * qm;
+          if constexpr (KV8) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = fmaf(z[j], k, ts.y);
+            for (int j = 0; j < 32; j += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(sc + j);
+              z[j] = fmaf(z[j] * f.x, k, ts.y);
+              z[j + 1] = fmaf(z[j + 1] * f.y, k, ts.y);
+              z[j + 2] = fmaf(z[j + 2] * f.z, k, ts.y);
+              z[j + 3] = fmaf(z[j + 3] * f.w, k, ts.y);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z[j] *= k;
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) z[j] = fmaf(z[j] * qm, sc[j] * a.scale_log2, __log2f(sc[j]));
@@ -902,6 +927,17 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         if (one) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) sums[j & 3] += z[j];
+          if constexpr (KV8) {
+            // the values are codes: P takes their scales, over the tile's
+#pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(sc + j);
+              z[j] *= f.x;
+              z[j + 1] *= f.y;
+              z[j + 2] *= f.z;
+              z[j + 3] *= f.w;
+            }
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) sums[j & 3] += __fdividef(z[j], sc[j]);
@@ -995,30 +1031,27 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       a.desc[2 * pair + 1] = head_q;
     }
     __syncwarp();
-  } else if (KV8) {
-    // ------------------------------------------------------------ e4m3: codes widened, queries scaled
-    // In the order of the MMAs: the keys of a tile, two chunks at a time, then
-    // the values of the tile before.  thread: 16 codes of two tokens.  Lanes of
-    // odd chunks store their two pieces in the other order, so that the eight
-    // lanes of a store lie in different banks.
+  } else if (KV8 && warp < SMX0 + SMX + GROUP) {
+    // ------------------------------------------------------------ e4m3: keys widened, queries scaled
+    // Two chunks at a time.  thread: 16 codes of four tokens; those of the next
+    // chunks come to registers while these are widened.  Lanes of odd chunks store
+    // their two pieces in the other order, so that the eight lanes of a store lie
+    // in different banks.
     const int lw = warp - (SMX0 + SMX);
     const int lt = lw * 32 + lane;
+    const int pc = lt & 7, r0 = lt >> 3, flip = pc >> 2, rp = lt >> 2;
     bool ok = true;
-    int q = q0, off = off0, left = ntile, n = 0, u = 0;
+    int off = off0, left = ntile, n = 0, u = 0, q = q0;
     uint32_t seg = 0;
-    Ring<VR> vr;
-    Ring<VUR> ur;
-
     auto query = [&]() {
       if (!(ok = ok && await(q_raw, seg & 1, a.err))) return;
-      scale_query(qs, qmul + (seg & 1) * RH, HC >> 3, lw, lane);
+      scale_query(qs, qmul + (seg & 1) * RH, HC >> 2, lw, lane);
       hand_over(q_full);
     };
-
+    uint8_t* const dst = ks + flip * CH + r0 * 128;
 #pragma unroll 1
-    for (int g = 0; g <= ntile && ok; ++g) {
-      const bool first = u == n;                     // tile g is a segment's first
-      if (first && g < ntile) {
+    for (int g = 0; g < ntile && ok; ++g) {
+      if (u == n) {
         if (g > 0) {
           ++q;
           ++seg;
@@ -1027,77 +1060,75 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         n = min(tiles_of<IDX>(a, q) - off, left);
         left -= n;
         u = 0;
+        if (g == 0) query();                         // while its rows are looked up
       }
-      // the MMAs finish a segment's values before the next one's scores
+      if (!(ok = ok && await(&ku_full[0], g & 1, a.err))) break;
+      const uint8_t* src = smem + L::OFF_KU + r0 * 256 + pc * 16;
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = lds16(src + i * 16 * 256);
 #pragma unroll 1
-      for (int turn = 0; turn < 2 && ok; ++turn) {
-        if ((turn == 0) != first) {
-          if (g == ntile) continue;
-          const uint32_t slot = g % RR;
-          // the first query while its rows are looked up, others when the slots of
-          // their keys are full
-          if (g == 0) query();
-          if (!(ok = ok && await(&r_full[slot], (g / RR) & 1, a.err))) break;
-          const __half2* fs = fold + slot * NT + half * NH;
-          const int pc = lt & 7, r0 = lt >> 3, flip = pc >> 2;
-          const __half2 f0 = fs[r0], f1 = fs[r0 + 32];
-#pragma unroll 1
-          for (int d = 0; d < 4; ++d) {
-            if (first && g > 0 && d == 2) query();
-            if ((d & 1) == 0) ok = ok && await(&ku_full[d >> 1], g & 1, a.err);
-            const uint8_t* src = smem + L::OFF_KU + (d >> 1) * KUB + (d & 1) * 128 + r0 * 256 + pc * 16;
-            const uint4 v0 = lds16(src), v1 = lds16(src + 32 * 256);
-            if (!(ok = ok && await(&k_empty[d & 1], key_use(d, g) ^ 1, a.err))) break;
-            uint8_t* dst = ks + (2 * (d & 1) + flip) * CH + r0 * 128;
-            store_wide(dst, 2 * (pc & 3), r0 & 7, flip, v0, f0);
-            store_wide(dst + 32 * 128, 2 * (pc & 3), r0 & 7, flip, v1, f1);
-            hand_over(&k_full[d & 1]);
-            if ((d & 1) && lane == 0) mbar_arrive(&ku_empty[d >> 1]);   // only now: the stores have waited for the loads
-            __syncwarp();
-          }
-          ok = ok && await(&ku_full[2], g & 1, a.err);
-          const int rp = lt >> 2;
-          const uint4 v = lds16(smem + L::OFF_KU + 2 * KUB + lt * 16);
-          if (!(ok = ok && await(&k_empty[2], (g & 1) ^ 1, a.err))) break;
-          store_wide(ks + 4 * CH + rp * 128, 2 * (lt & 3), rp & 7, 0, v, fs[rp]);
-          hand_over(&k_full[2]);
-          if (lane == 0) mbar_arrive(&ku_empty[2]);
-          __syncwarp();
-          ++u;
-        } else if (g > 0) {
-          const uint32_t slot = (g - 1) % RR;
-          const int pc = lt & 15, r0 = lt >> 4, flip = pc >> 2 & 1;
-          const __half2* fs = fold + slot * NT + r0;
-#pragma unroll 1
-          for (int c = 0; c < VS; ++c, fs += VT) {
-            ok = ok && await(&vu_full[ur.slot], ur.use, a.err);
-            const uint8_t* src = smem + L::OFF_VU + ur.slot * VUB + lt * 16;
-            const uint4 v0 = lds16(src), v1 = lds16(src + 16 * 256);
-            const __half2 f0 = fs[0], f1 = fs[16];
-            if (!(ok = ok && await(&v_empty[vr.slot], vr.use ^ 1, a.err))) break;
-            uint8_t* dst = vs + vr.slot * VSLOT + (pc >> 2) * VCH + r0 * 128;
-            store_wide(dst, 2 * (pc & 3), r0 & 7, flip, v0, f0);
-            store_wide(dst + VSTEP, 2 * (pc & 3), r0 & 7, flip, v1, f1);
-            hand_over(&v_full[vr.slot]);
-            if (lane == 0) mbar_arrive(&vu_empty[ur.slot]);
-            __syncwarp();
-            vr.next();
-            ur.next();
-          }
-          if (lane == 0) mbar_arrive(&r_empty[slot]);
-          __syncwarp();
+      for (int d = 0; d < 4; ++d) {
+        const bool free = mbar_test_wait(&k_empty[d & 1], (d >> 1) ^ 1);
+        if (d & 1) ok = ok && await(&ku_full[(d + 1) >> 1], g & 1, a.err);
+        src += d & 1 ? KUB - 128 : 128;
+        if (u == 0 && g > 0 && d == 2) query();      // both slots are full: their scores wait for the query
+        if (!(ok = ok && (__all_sync(0xffffffffu, free) || await(&k_empty[d & 1], (d >> 1) ^ 1, a.err)))) break;
+        uint8_t* to = dst + (d & 1) * 2 * CH;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 c = v[i];
+          if (d < 3) v[i] = lds16(src + i * 16 * 256);
+          else if (i < 2) v[i] = lds16(smem + L::OFF_KU + 2 * KUB + rp * 64 + (lt & 3) * 16 + i * 32 * 64);
+          store_wide(to + i * 16 * 128, 2 * (pc & 3), r0 & 7, flip, c);
         }
+        hand_over(&k_full[d & 1]);
+        if ((d & 1) && lane == 0) mbar_arrive(&ku_empty[d >> 1]);   // only now: the stores have waited for the loads
+        __syncwarp();
       }
+      if (!(ok = ok && await(&k_empty[2], (g & 1) ^ 1, a.err))) break;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        store_wide(ks + 4 * CH + (rp + 32 * i) * 128, 2 * (lt & 3), rp & 7, 0, v[i]);
+      hand_over(&k_full[2]);
+      if (lane == 0) mbar_arrive(&ku_empty[2]);
+      __syncwarp();
+      ++u;
     }
-    // the MMAs have read every key and value
-    if (ok && ntile > 0) {
-      ok = await<true>(&k_empty[0], 1, a.err) && await<true>(&k_empty[1], 1, a.err) &&
-           await<true>(&k_empty[2], (ntile - 1) & 1, a.err);
+    // the MMAs have read every key
+    if (ok && ntile > 0)
+      ok = await(&k_empty[0], 1, a.err) && await(&k_empty[1], 1, a.err) && await(&k_empty[2], (ntile - 1) & 1, a.err);
+  } else if (KV8) {
+    // ------------------------------------------------------------ e4m3: values widened
+    // A unit at a time.  thread: 16 codes of four tokens, as above.
+    const int lt = (warp - (SMX0 + SMX + GROUP)) * 32 + lane;
+    const int pc = lt & 15, r0 = lt >> 4, flip = (pc >> 2) & 1;
+    bool ok = true;
+    Ring<VR> vr;
+    Ring<VUR> ur;
 #pragma unroll 1
-      for (int i = 0; i < VR && ok; ++i) {
-        ok = await<true>(&v_empty[vr.slot], vr.use ^ 1, a.err);
-        vr.next();
-      }
+    for (int c = 0; c < ntile * VS && ok; ++c) {
+      const bool free = mbar_test_wait(&v_empty[vr.slot], vr.use ^ 1);
+      if (!(ok = await(&vu_full[ur.slot], ur.use, a.err))) break;
+      const uint8_t* src = smem + L::OFF_VU + ur.slot * VUB + lt * 16;
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = lds16(src + i * 8 * 256);
+      if (!(ok = __all_sync(0xffffffffu, free) || await(&v_empty[vr.slot], vr.use ^ 1, a.err))) break;
+      uint8_t* dst = vs + vr.slot * VSLOT + (pc >> 2) * VCH + r0 * 128;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) store_wide(dst + (i >> 1) * VSTEP + (i & 1) * 1024, 2 * (pc & 3), r0 & 7, flip, v[i]);
+      hand_over(&v_full[vr.slot]);
+      if (lane == 0) mbar_arrive(&vu_empty[ur.slot]);
+      __syncwarp();
+      vr.next();
+      ur.next();
+    }
+    // the MMAs have read every value
+#pragma unroll 1
+    for (int i = 0; i < VR && ok && ntile > 0; ++i) {
+      ok = await(&v_empty[vr.slot], vr.use ^ 1, a.err);
+      vr.next();
     }
   }
 
