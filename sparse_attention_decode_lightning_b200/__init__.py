@@ -250,40 +250,79 @@ def dsa_sparse_mla_decode_fp8(q, kv_pool, kv_scale, page_table, q_offsets, q_vis
         _ptr(ws), ws.numel(), _stream(stream)), "dsa_sparse_mla_decode_fp8")
 
 
-def _rows_ptr(t: torch.Tensor, width: int, dtype, name: str):
-    """Pointer of a [T, width] device tensor whose rows may be apart."""
-    if not t.is_cuda:
+# The calls below cost a decode step a few microseconds of host time each, so
+# they check their arguments once, with few operations on each tensor.
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _device_of(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("libdsa takes device tensors")
-    if t.dtype != dtype or t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
-        raise ValueError(f"{name}: [T, {width}] {dtype} with dense rows")
-    return ctypes.c_void_p(t.data_ptr())
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
+    return dev
 
 
-def _expect(name: str, t: torch.Tensor, dtype, *shape):
-    """Type and shape (None: any) of a tensor, on the current device."""
-    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
-    if t.dtype not in dtypes or t.dim() != len(shape) or any(w is not None and w != n for n, w in
-                                                            zip(t.shape, shape)):
+def _bad(name: str, t: torch.Tensor, dtype, shape, dev: int):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the others are on cuda:{dev}")
+    raise ValueError(f"{name}: libdsa takes contiguous tensors")
 
 
-def _cache(kv_pool, kv_scales, page_table, q_offsets, q_vis, rows: int, B: int):
-    """Checks the latent cache and the bookkeeping of a call; returns the tokens
-    that share a scale (1 for a bf16 cache)."""
-    e4m3 = (torch.uint8, torch.float8_e4m3fn)
-    _expect("kv_pool", kv_pool, torch.bfloat16 if kv_scales is None else e4m3, None, None, DIM)
-    _expect("page_table", page_table, torch.int32, B, None)
-    _expect("q_offsets", q_offsets, torch.int32, B + 1)
-    _expect("q_vis", q_vis, torch.int32, rows)
+def _at(name: str, t: torch.Tensor, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of this type and shape on device `dev`."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    _bad(name, t, dtype, shape, dev)
+
+
+def _rows_at(name: str, t: torch.Tensor, width: int, dev: int) -> int:
+    """Address of a bf16 [T, width] tensor whose rows may be apart."""
+    if t.dtype is not _BF16 or t.dim() != 2 or t.shape[1] != width or t.stride(1) != 1:
+        raise ValueError(f"{name}: [T, {width}] {_BF16} with dense rows")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the others are on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _ws_at(ws: torch.Tensor, dev: int):
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous tensor on cuda:{dev}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _raw_stream(stream, dev: int) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _cache(kv_pool, kv_scales, page_table, q_offsets, q_vis, rows: int, B: int, dev: int):
+    """Checks the latent cache and the bookkeeping of a call; returns the C call's
+    (pool, scales, num_pages, page_size, tokens of a scale), (table, max_pages), offsets, vis."""
+    if kv_pool.dim() != 3:
+        raise ValueError("kv_pool: [num_pages, page_size, 576]")
+    pages, page = kv_pool.shape[0], kv_pool.shape[1]
+    shape = (pages, page, DIM)
     if kv_scales is None:
-        return 1
-    _expect("kv_scales", kv_scales, torch.float32, kv_pool.shape[0], None)
-    n = kv_scales.shape[1]
-    if n == 0 or kv_pool.shape[1] % n:
-        raise ValueError("kv_scales: [num_pages, page_size / block]")
-    return kv_pool.shape[1] // n
+        pool, scales, block = _at("kv_pool", kv_pool, _BF16, shape, dev), None, 1
+    else:
+        if kv_pool.dtype not in _E4M3:
+            raise ValueError(f"kv_pool: expected {_E4M3}, got {kv_pool.dtype}")
+        pool = _at("kv_pool", kv_pool, kv_pool.dtype, shape, dev)
+        n = kv_scales.shape[1] if kv_scales.dim() == 2 else 0
+        if n == 0 or page % n:
+            raise ValueError("kv_scales: [num_pages, page_size / block]")
+        scales, block = _at("kv_scales", kv_scales, _F32, (pages, n), dev), page // n
+    if page_table.dim() != 2:
+        raise ValueError("page_table: [B, max_pages]")
+    max_pages = page_table.shape[1]
+    return ((pool, scales, pages, page, block), (_at("page_table", page_table, _I32, (B, max_pages), dev), max_pages),
+            _at("q_offsets", q_offsets, _I32, (B + 1,), dev), _at("q_vis", q_vis, _I32, (rows,), dev))
 
 
 def dsa_latent_append(kv, k_pe, inv_freq, kv_pool, page_table, q_offsets, q_vis, B, ws,
@@ -293,20 +332,22 @@ def dsa_latent_append(kv, k_pe, inv_freq, kv_pool, page_table, q_offsets, q_vis,
     [T,64] bf16 may be slices of one projection's output.  kv_scales (fp32
     [num_pages, page_size / block]) makes it an e4m3 cache with a scale for each
     block of tokens; see include/dsa.h."""
+    dev = _device_of(kv)
+    p_kv, p_pe = _rows_at("kv", kv, DIM_V, dev), _rows_at("k_pe", k_pe, DIM - DIM_V, dev)
     T = kv.shape[0]
-    p_kv = _rows_ptr(kv, DIM_V, torch.bfloat16, "kv")
-    p_pe = _rows_ptr(k_pe, DIM - DIM_V, torch.bfloat16, "k_pe")
-    _expect("kv", kv, torch.bfloat16, T, DIM_V)
-    _expect("k_pe", k_pe, torch.bfloat16, T, DIM - DIM_V)
-    _expect("inv_freq", inv_freq, torch.float32, (DIM - DIM_V) // 2)
-    block = _cache(kv_pool, kv_scales, page_table, q_offsets, q_vis, T, B)
+    if k_pe.shape[0] != T:
+        raise ValueError(f"k_pe: expected {T} rows, got {k_pe.shape[0]}")
+    freq = _at("inv_freq", inv_freq, _F32, ((DIM - DIM_V) // 2,), dev)
+    (pool, scales, pages, page, block), (table, max_pages), off, vis = _cache(kv_pool, kv_scales, page_table, q_offsets,
+                                                                              q_vis, T, B, dev)
     # a single row's stride says nothing about the rows after it
     ld_kv, ld_pe = (kv.stride(0), k_pe.stride(0)) if T > 1 else (DIM_V, DIM - DIM_V)
-    _check(lib().dsa_latent_append(
-        p_kv, ld_kv, p_pe, ld_pe, _ptr(inv_freq), int(interleaved), _ptr(page_table),
-        page_table.shape[1], _ptr(q_offsets), _ptr(q_vis), B, T, _ptr(kv_pool), _ptr(kv_scales),
-        kv_pool.shape[0], kv_pool.shape[1], block, _ptr(ws), ws.numel() * ws.element_size(),
-        _stream(stream)), "dsa_latent_append")
+    p_ws, n_ws = _ws_at(ws, dev)
+    status = (_lib or lib()).dsa_latent_append(p_kv, ld_kv, p_pe, ld_pe, freq, 1 if interleaved else 0, table, max_pages, off,
+                                               vis, B, T, pool, scales, pages, page, block, p_ws, n_ws,
+                                               _raw_stream(stream, dev))
+    if status:
+        raise DSAError(status, "dsa_latent_append")
 
 
 def dsa_attend_workspace_bytes(heads: int) -> int:
@@ -322,38 +363,43 @@ def attend_workspace(heads: int = HEADS, device="cuda") -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device)
 
 
-def _attend_args(q, kv_pool, kv_scales, page_table, q_offsets, q_vis, B, out, lse):
-    Q, H = q.shape[0], q.shape[1]
-    _expect("q", q, torch.bfloat16, None, None, DIM)
-    _expect("out", out, torch.bfloat16, Q, H, DIM_V)
-    _expect("lse", lse, torch.float32, Q, H)
-    return Q, H, _cache(kv_pool, kv_scales, page_table, q_offsets, q_vis, Q, B)
-
-
 def dsa_mla_decode_sinks(q, kv_pool, page_table, q_offsets, q_vis, B, sinks, window, scale, out,
                          lse, ws, kv_scales=None, stream=None):
     """MLA decode over the first `sinks` and the last `window` visible tokens, of a
     bf16 cache or (kv_scales) a block-scaled e4m3 one; out bf16 [Q,heads,512],
     lse fp32 [Q,heads]; see include/dsa.h."""
-    Q, H, block = _attend_args(q, kv_pool, kv_scales, page_table, q_offsets, q_vis, B, out, lse)
-    _check(lib().dsa_mla_decode_sinks(
-        _ptr(q), _ptr(kv_pool), _ptr(kv_scales), kv_pool.shape[0], kv_pool.shape[1], block,
-        _ptr(page_table), page_table.shape[1], _ptr(q_offsets), _ptr(q_vis), B, Q, H, sinks, window,
-        float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(),
-        _stream(stream)), "dsa_mla_decode_sinks")
+    dev = _device_of(q)
+    if q.dim() != 3:
+        raise ValueError("q: [Q, heads, 576]")
+    Q, H = q.shape[0], q.shape[1]
+    (pool, scales, pages, page, block), (table, max_pages), off, vis = _cache(kv_pool, kv_scales, page_table, q_offsets,
+                                                                              q_vis, Q, B, dev)
+    p_ws, n_ws = _ws_at(ws, dev)
+    status = (_lib or lib()).dsa_mla_decode_sinks(
+        _at("q", q, _BF16, (Q, H, DIM), dev), pool, scales, pages, page, block, table, max_pages, off, vis, B, Q, H, sinks,
+        window, scale, _at("out", out, _BF16, (Q, H, DIM_V), dev), _at("lse", lse, _F32, (Q, H), dev), p_ws, n_ws,
+        _raw_stream(stream, dev))
+    if status:
+        raise DSAError(status, "dsa_mla_decode_sinks")
 
 
 def dsa_sparse_mla_decode_fp8_block(q, kv_pool, kv_scales, page_table, q_offsets, q_vis, idx, B,
                                     scale, out, lse, ws, stream=None):
     """Sparse MLA over the selected tokens of a block-scaled e4m3 cache; out bf16
     [Q,heads,512], lse fp32 [Q,heads]; see include/dsa.h."""
-    Q, H, block = _attend_args(q, kv_pool, kv_scales, page_table, q_offsets, q_vis, B, out, lse)
-    _expect("idx", idx, torch.int32, Q, None)
-    _check(lib().dsa_sparse_mla_decode_fp8_block(
-        _ptr(q), _ptr(kv_pool), _ptr(kv_scales), kv_pool.shape[0], kv_pool.shape[1], block,
-        _ptr(page_table), page_table.shape[1], _ptr(q_offsets), _ptr(q_vis), _ptr(idx), B, Q, H,
-        idx.shape[1], float(scale), _ptr(out), _ptr(lse), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream)), "dsa_sparse_mla_decode_fp8_block")
+    dev = _device_of(q)
+    if q.dim() != 3 or idx.dim() != 2 or kv_scales is None:
+        raise ValueError("q: [Q, heads, 576], idx: [Q, topk], kv_scales: [num_pages, page_size / block]")
+    Q, H, topk = q.shape[0], q.shape[1], idx.shape[1]
+    (pool, scales, pages, page, block), (table, max_pages), off, vis = _cache(kv_pool, kv_scales, page_table, q_offsets,
+                                                                              q_vis, Q, B, dev)
+    p_ws, n_ws = _ws_at(ws, dev)
+    status = (_lib or lib()).dsa_sparse_mla_decode_fp8_block(
+        _at("q", q, _BF16, (Q, H, DIM), dev), pool, scales, pages, page, block, table, max_pages, off, vis,
+        _at("idx", idx, _I32, (Q, topk), dev), B, Q, H, topk, scale, _at("out", out, _BF16, (Q, H, DIM_V), dev),
+        _at("lse", lse, _F32, (Q, H), dev), p_ws, n_ws, _raw_stream(stream, dev))
+    if status:
+        raise DSAError(status, "dsa_sparse_mla_decode_fp8_block")
 
 
 def dsa_lse_combine(o_parts, lse_parts, out, lse, stream=None):
