@@ -77,6 +77,7 @@ constexpr int KUB = NH * 256;                        // bytes of a wide unit
 constexpr int VUB = VT * 256;                        // bytes of a value unit's codes
 constexpr int VUR = 2;                               // units of their ring
 constexpr int RUN = 16;                              // rows that one load can bring where they are consecutive
+constexpr int START = 2;                              // tiles that beginning a query costs
 constexpr int RR = 3;                                // tiles looked up ahead
 constexpr int SMX = 8;                               // softmax warps
 constexpr int GROUP = 4;                             // warps that widen keys; as many widen values
@@ -105,8 +106,8 @@ struct Plan {
   static constexpr int OFF_RUNS = OFF_MASK + RR * 4 * 4;             // uint32 [4]: bit i: rows 16 i .. 16 i + 15 are consecutive, or none is held
   static constexpr int OFF_QMUL = OFF_RUNS + 16;                     // float [2][64], by segment
   static constexpr int OFF_MX = OFF_QMUL + 2 * RH * 4;               // float [2][4][64]: between the parts of a row
-  static constexpr int OFF_SCAN = OFF_MX + 8 * RH * 4;               // int64 [20], then the first query and its tile
-  static constexpr int OFF_BAR = OFF_SCAN + 22 * 8;
+  static constexpr int OFF_SCAN = OFF_MX + 8 * RH * 4;               // int64 [20]; the share's first and last tile; its first query and that one's tile
+  static constexpr int OFF_BAR = OFF_SCAN + 24 * 8;
   static constexpr int NBAR = 2 * RR + 2 * KS + 2 * VR + 2 + 4 + (KV8 ? 1 + 2 * KU + 2 * VUR : 0);
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16;
@@ -458,7 +459,8 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   if (warp == 0) tmem_alloc_pair(tmem_holder, TMEM_COLS);
 
   // This pair's share [t0, t1) of all tiles: a thread sums the tiles of some
-  // consecutive queries, the block scans the sums.
+  // consecutive queries, the block scans the sums.  Where there is enough of
+  // them a query counts START tiles more, about what it costs to begin one.
   const int per = (a.Q + THREADS - 1) / THREADS;
   const int qa = min(a.Q, tid * per), qb = min(a.Q, qa + per);
   int64_t sum = 0;
@@ -471,6 +473,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     if (lane >= o) incl += v;
   }
   if (lane == 31) scan[warp] = incl;
+  if (tid < 2) scan[20 + tid] = 0;
   __syncthreads();
   int64_t base = 0, total = 0;
 #pragma unroll 1
@@ -479,28 +482,46 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     total += scan[w];
   }
   base += incl - sum;
+  const int start = total >= 4 * pairs ? START : 0;
   const uint32_t np = total < pairs ? static_cast<uint32_t>(total) : pairs;   // pairs that get work
-  const int64_t each = total >> 32 ? total / np : static_cast<uint32_t>(total) / np;
-  const uint32_t over = static_cast<uint32_t>(total - each * np);
-  const uint32_t up = pair;
-  const int64_t t0 = up < np ? each * up + min(up, over) : 0;
-  const int64_t t1 = up < np ? t0 + each + (up < over ? 1 : 0) : 0;
-  if (t1 > t0 && t0 >= base && t0 < base + sum) {
-    int64_t at = base;
-    int q = qa;
+  const int64_t cost = total + static_cast<int64_t>(start) * a.Q;
+  const int64_t each = cost >> 32 ? cost / np : static_cast<uint32_t>(cost) / np;
+  const uint32_t over = static_cast<uint32_t>(cost - each * np);
+  // where the shares of this pair and of the next one begin
 #pragma unroll 1
-    for (int n; at + (n = tiles_of<IDX>(a, q)) <= t0; ++q) at += n;
-    scan[20] = q;
-    scan[21] = t0 - at;
+  for (uint32_t i = 0; i < 2; ++i) {
+    const uint32_t p = min(pair + i, np);
+    const int64_t c = p == np ? cost : each * p + min(p, over);
+    if (p == np) {
+      if (tid == 0) scan[20 + i] = total;
+    } else {
+      int64_t at = base;
+      const int64_t at_cost = base + static_cast<int64_t>(start) * qa;
+      if (c >= at_cost && c < at_cost + sum + static_cast<int64_t>(start) * (qb - qa)) {
+        int64_t left = c - at_cost;
+        int q = qa;
+#pragma unroll 1
+        for (int n; left >= start + (n = tiles_of<IDX>(a, q)); ++q) {
+          left -= start + n;
+          at += n;
+        }
+        const int64_t off = left > start ? left - start : 0;
+        scan[20 + i] = at + off;
+        if (i == 0) {
+          scan[22] = q;
+          scan[23] = off;
+        }
+      }
+    }
   }
-  if (half == 0 && tid < 2 && t1 == t0) a.desc[2 * pair + tid] = -1;
   tc_fence_before();
   cluster_sync();                                    // both CTAs' barriers and tensor memory are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int q0 = static_cast<int>(scan[20]);
-  const int off0 = static_cast<int>(scan[21]);
-  const int ntile = static_cast<int>(t1 - t0);
+  const int q0 = static_cast<int>(scan[22]);
+  const int off0 = static_cast<int>(scan[23]);
+  const int ntile = static_cast<int>(scan[21] - scan[20]);
+  if (half == 0 && tid < 2 && ntile == 0) a.desc[2 * pair + tid] = -1;
 
   // the first CTA's barrier of the same name
   auto leader = [&](uint64_t* bar) { return map_to_rank(smem_u32(bar), 0); };
@@ -657,7 +678,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
               for (int c = 0; c < KCH; ++c) gather4_pair(dst + c * 1024, &maps.row, 64 * (KCH * j + c), r, bar);
             }
             __syncwarp();
-            if (lane < 16 && run && (t & 1) == 0) load_3d_pair(dst, &maps.run, r0 < 0 ? r0 : static_cast<int>(r.x), KCH * j, bar);
+            if (lane < 16 && run && (t & 1) == 0) load_3d_pair(dst, &maps.run, r0, KCH * j, bar);
           }
           __syncwarp();
         }
