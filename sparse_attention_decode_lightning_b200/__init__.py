@@ -260,7 +260,7 @@ def _device_of(t: torch.Tensor) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError("libdsa takes device tensors")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():            # a device tensor exists, so CUDA is initialised
         raise ValueError(f"the tensors are on cuda:{dev}, which is not the current device")
     return dev
 

@@ -11,10 +11,14 @@
 // only where it falls into e4m3's subnormals).
 //
 // The angle: p * inv_freq exceeds what fp32 resolves for far positions (1e6
-// rad has a spacing of 1/16), so it is formed in fp64 as turns, reduced to
-// [-1/2, 1/2] there, and only then rounded to fp32 for sincospi.
+// rad has a spacing of 1/16).  A lane keeps its turns a position, modulo 1, as a
+// fraction of 2^64; p times that wraps as the angle does, and its upper half is
+// the angle to 2^-32 of a turn.
 //
-// Bound: bytes (1152 read, 576 or 1152 written a token).
+// Bound: bytes (1152 read, 576 or 1152 written a token).  The sixteen warps that
+// share a run hold its rows in registers between the maximum and the rounding,
+// up to four a warp, so a row is read once and all its loads are under way at
+// once; longer runs (blocks of more than 64 tokens) are read twice.
 #include "common.cuh"
 #include "internal.h"
 
@@ -23,10 +27,9 @@
 namespace dsa {
 namespace {
 
-constexpr int WARPS = 8;
-constexpr int THREADS = 32 * WARPS;
 constexpr int MAX_G = 64;                  // rows of the token array a CTA looks for run starts in
 constexpr int EXP_LIMIT = 40;
+constexpr int KEEP = 4;                    // rows of a run that a warp holds in registers
 
 struct AppendArgs {
   const __nv_bfloat16* kv;
@@ -48,21 +51,39 @@ struct Row {
   float x, y;
 };
 
-__device__ __forceinline__ Row load_row(const AppendArgs& A, int t, int pos, float inv_freq, int lane) {
+// turns a position modulo 1, in 2^-64; a frequency that is no number has no angle
+struct Freq {
+  uint64_t step;
+  float bad;                               // 0, or NaN
+};
+
+__device__ __forceinline__ Freq turns_of(float inv_freq) {
+  Freq f;
+  double t = static_cast<double>(inv_freq) * 0.15915494309189535;
+  f.bad = inv_freq - inv_freq;
+  t -= rint(t);                            // [-1/2, 1/2]
+  f.step = f.bad == 0.f ? static_cast<uint64_t>(__double2ll_rn(t * 9223372036854775808.0)) << 1 : 0;
+  return f;
+}
+
+__device__ __forceinline__ Row load_row(const AppendArgs& A, int t, int lane) {
   Row r;
   const uint4* src = reinterpret_cast<const uint4*>(A.kv + static_cast<int64_t>(t) * A.ld_kv) + 2 * lane;
   r.a = __ldg(src);
   r.b = __ldg(src + 1);
   const __nv_bfloat16* pe = A.k_pe + static_cast<int64_t>(t) * A.ld_pe;
-  const float x = __bfloat162float(pe[A.interleaved ? 2 * lane : lane]);
-  const float y = __bfloat162float(pe[A.interleaved ? 2 * lane + 1 : lane + 32]);
-  double turns = static_cast<double>(pos) * static_cast<double>(inv_freq) * 0.15915494309189535;
-  turns -= rint(turns);
-  float s, c;
-  sincospif(2.f * static_cast<float>(turns), &s, &c);
-  r.x = x * c - y * s;
-  r.y = y * c + x * s;
+  r.x = __bfloat162float(pe[A.interleaved ? 2 * lane : lane]);
+  r.y = __bfloat162float(pe[A.interleaved ? 2 * lane + 1 : lane + 32]);
   return r;
+}
+
+__device__ __forceinline__ void rotate(Row& r, int pos, const Freq& f) {
+  const int32_t turns = static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(pos)) * f.step) >> 32);
+  float s, c;
+  sincospif(fmaf(static_cast<float>(turns), 0x1p-31f, f.bad), &s, &c);
+  const float x = r.x;
+  r.x = x * c - r.y * s;
+  r.y = r.y * c + x * s;
 }
 
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
@@ -79,11 +100,23 @@ __device__ __forceinline__ float mag4(uint4 v) {
                fmaxf(fmaxf(mag(lo_f(v.z)), mag(hi_f(v.z))), fmaxf(mag(lo_f(v.w)), mag(hi_f(v.w)))));
 }
 
-__device__ __forceinline__ float row_amax(const Row& r) {
-  float m = fmaxf(fmaxf(mag4(r.a), mag4(r.b)), fmaxf(mag(r.x), mag(r.y)));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  return m;
+__device__ __forceinline__ uint32_t pair_bits(uint32_t m, uint32_t w) {
+  return max(max(m, (w << 16) & 0x7FFF0000u), w & 0x7FFF0000u);
+}
+
+// a lane's largest magnitude of a row, and whether all its values are finite:
+// the magnitudes compare as integers, and what is not finite as the largest
+__device__ __forceinline__ float lane_amax(const Row& r, bool* finite) {
+  uint32_t m = max(__float_as_uint(fabsf(r.x)), __float_as_uint(fabsf(r.y)));
+  m = pair_bits(pair_bits(pair_bits(pair_bits(m, r.a.x), r.a.y), r.a.z), r.a.w);
+  m = pair_bits(pair_bits(pair_bits(pair_bits(m, r.b.x), r.b.y), r.b.z), r.b.w);
+  *finite = m < 0x7F800000u;
+  if (*finite) return __uint_as_float(m);
+  return fmaxf(fmaxf(mag4(r.a), mag4(r.b)), fmaxf(mag(r.x), mag(r.y)));
+}
+
+__device__ __forceinline__ float warp_max(float m) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));   // m >= 0
 }
 
 // smallest e in [-40, 40] with amax <= 448 * 2^e = 1.75 * 2^(e + 8)
@@ -103,9 +136,27 @@ __device__ __forceinline__ uint32_t f8(float v) {
   return __nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3);
 }
 
-__device__ __forceinline__ uint32_t f8x4(uint32_t w0, uint32_t w1, float s) {
+__device__ __forceinline__ uint32_t f8_div4(uint32_t w0, uint32_t w1, float s) {
   return f8(__fdiv_rn(lo_f(w0), s)) | (f8(__fdiv_rn(hi_f(w0), s)) << 8) |
          (f8(__fdiv_rn(lo_f(w1), s)) << 16) | (f8(__fdiv_rn(hi_f(w1), s)) << 24);
+}
+
+// four values times inv, a power of two: scaling is exact but for subnormals, as
+// the division would be
+__device__ __forceinline__ uint32_t f8x4(uint32_t w0, uint32_t w1, float inv, bool finite) {
+  const float a = lo_f(w0) * inv, b = hi_f(w0) * inv, c = lo_f(w1) * inv, d = hi_f(w1) * inv;
+  if (finite)
+    return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3)) |
+           static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3)) << 16;
+  return f8(a) | (f8(b) << 8) | (f8(c) << 16) | (f8(d) << 24);
+}
+
+__device__ __forceinline__ void store_e4m3(const AppendArgs& A, int64_t slot, const Row& w, float inv, bool finite, int lane) {
+  uint8_t* dst = A.pool + slot * DSA_DIM;
+  reinterpret_cast<uint4*>(dst)[lane] = make_uint4(f8x4(w.a.x, w.a.y, inv, finite), f8x4(w.a.z, w.a.w, inv, finite),
+                                                   f8x4(w.b.x, w.b.y, inv, finite), f8x4(w.b.z, w.b.w, inv, finite));
+  dst[DSA_DIM_V + (A.interleaved ? 2 * lane : lane)] = static_cast<uint8_t>(f8(w.x * inv));
+  dst[DSA_DIM_V + (A.interleaved ? 2 * lane + 1 : lane + 32)] = static_cast<uint8_t>(f8(w.y * inv));
 }
 
 __device__ __forceinline__ float f8_value(uint32_t code) {
@@ -165,10 +216,11 @@ __device__ __forceinline__ Run find_run(const AppendArgs& A, const int* off, int
   return r;
 }
 
-// W warps a run: 1 where runs are short (decode, small blocks), 8 where they
-// are long.  One row a warp at a time.
+// W warps a run: 1 of a CTA's 8 where runs are short (decode, small blocks), all
+// 16 where they are long.
 template <bool KV8, int W>
-__global__ void __launch_bounds__(THREADS) latent_append_kernel(const __grid_constant__ AppendArgs A) {
+__global__ void __launch_bounds__(W == 1 ? 256 : 512, W == 1 ? 1 : 2) latent_append_kernel(const __grid_constant__ AppendArgs A) {
+  constexpr int WARPS = W == 1 ? 8 : W, THREADS = 32 * WARPS;
   __shared__ int off[DSA_MAX_BATCH + 1];
   __shared__ Run runs[MAX_G];
   __shared__ int n_runs;
@@ -185,7 +237,7 @@ __global__ void __launch_bounds__(THREADS) latent_append_kernel(const __grid_con
     }
   }
   __syncthreads();
-  const float inv_freq = A.inv_freq[lane];
+  const Freq freq = turns_of(A.inv_freq[lane]);
   constexpr int GROUPS = WARPS / W;
   const int group = warp / W, wg = warp % W;
   for (int k = group; k < n_runs; k += GROUPS) {
@@ -197,7 +249,8 @@ __global__ void __launch_bounds__(THREADS) latent_append_kernel(const __grid_con
           if (v != 0 && lane == 0) raise_error(A.err, DEVERR_BOUNDS);
           continue;
         }
-        const Row w = load_row(A, r.t + i, r.pos + i, inv_freq, lane);
+        Row w = load_row(A, r.t + i, lane);
+        rotate(w, r.pos + i, freq);
         __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(A.pool) + (r.slot + i) * DSA_DIM;
         reinterpret_cast<uint4*>(dst)[2 * lane] = w.a;
         reinterpret_cast<uint4*>(dst)[2 * lane + 1] = w.b;
@@ -210,15 +263,46 @@ __global__ void __launch_bounds__(THREADS) latent_append_kernel(const __grid_con
       const float old = held ? *sp : 0.f;
       float m = 0.f;
       bool any = false;
-      for (int i = wg; i < r.n; i += W) {
-        const int v = A.q_vis[r.t + i];
-        if (v != r.vis0 + i) {
-          if (v != 0 && lane == 0) raise_error(A.err, DEVERR_BOUNDS);
-          continue;
+      Row keep[KEEP];
+      uint32_t kept = 0, odd = 0;                          // rows in registers; of them not finite in this lane
+      const bool held_back = r.n <= KEEP * W;              // every row stays in registers
+      if (held_back) {
+#pragma unroll
+        for (int j = 0; j < KEEP; ++j) {
+          const int i = wg + j * W;
+          if (i >= r.n) break;
+          const int v = A.q_vis[r.t + i];
+          if (v == r.vis0 + i) {
+            kept |= 1u << j;
+            keep[j] = load_row(A, r.t + i, lane);
+          } else if (v != 0 && lane == 0) {
+            raise_error(A.err, DEVERR_BOUNDS);
+          }
         }
-        any = true;
-        m = fmaxf(m, row_amax(load_row(A, r.t + i, r.pos + i, inv_freq, lane)));
+#pragma unroll
+        for (int j = 0; j < KEEP; ++j)
+          if (kept >> j & 1u) {
+            rotate(keep[j], r.pos + wg + j * W, freq);
+            bool finite;
+            m = fmaxf(m, lane_amax(keep[j], &finite));
+            odd |= finite ? 0u : 1u << j;
+          }
+        any = kept != 0;
+      } else {
+        for (int i = wg; i < r.n; i += W) {
+          const int v = A.q_vis[r.t + i];
+          if (v != r.vis0 + i) {
+            if (v != 0 && lane == 0) raise_error(A.err, DEVERR_BOUNDS);
+            continue;
+          }
+          any = true;
+          Row w = load_row(A, r.t + i, lane);
+          rotate(w, r.pos + i, freq);
+          bool finite;
+          m = fmaxf(m, lane_amax(w, &finite));
+        }
       }
+      m = warp_max(m);
       if constexpr (W > 1) {
         if (lane == 0) wmax[warp] = any ? m : -1.f;
         __syncthreads();
@@ -244,14 +328,29 @@ __global__ void __launch_bounds__(THREADS) latent_append_kernel(const __grid_con
           base[i] = c;
         }
       }
-      for (int i = wg; i < r.n; i += W) {
-        if (A.q_vis[r.t + i] != r.vis0 + i) continue;
-        const Row w = load_row(A, r.t + i, r.pos + i, inv_freq, lane);
-        uint8_t* dst = A.pool + (r.slot + i) * DSA_DIM;
-        reinterpret_cast<uint4*>(dst)[lane] = make_uint4(f8x4(w.a.x, w.a.y, s), f8x4(w.a.z, w.a.w, s),
-                                                         f8x4(w.b.x, w.b.y, s), f8x4(w.b.z, w.b.w, s));
-        dst[DSA_DIM_V + (A.interleaved ? 2 * lane : lane)] = static_cast<uint8_t>(f8(__fdiv_rn(w.x, s)));
-        dst[DSA_DIM_V + (A.interleaved ? 2 * lane + 1 : lane + 32)] = static_cast<uint8_t>(f8(__fdiv_rn(w.y, s)));
+      const float inv = __fdiv_rn(1.f, s);                 // exact where s is a power of two; an old scale may be none
+      const bool exact = (__float_as_uint(s) & 0x7FFFFFu) == 0;
+      if (held_back && exact) {
+#pragma unroll
+        for (int j = 0; j < KEEP; ++j)
+          if (kept >> j & 1u) store_e4m3(A, r.slot + wg + j * W, keep[j], inv, !(odd >> j & 1u), lane);
+      } else {
+        for (int i = wg; i < r.n; i += W) {
+          if (A.q_vis[r.t + i] != r.vis0 + i) continue;
+          Row w = load_row(A, r.t + i, lane);
+          rotate(w, r.pos + i, freq);
+          if (exact) {
+            bool finite;
+            lane_amax(w, &finite);
+            store_e4m3(A, r.slot + i, w, inv, finite, lane);
+          } else {
+            uint8_t* dst = A.pool + (r.slot + i) * DSA_DIM;
+            reinterpret_cast<uint4*>(dst)[lane] = make_uint4(f8_div4(w.a.x, w.a.y, s), f8_div4(w.a.z, w.a.w, s),
+                                                             f8_div4(w.b.x, w.b.y, s), f8_div4(w.b.z, w.b.w, s));
+            dst[DSA_DIM_V + (A.interleaved ? 2 * lane : lane)] = static_cast<uint8_t>(f8(__fdiv_rn(w.x, s)));
+            dst[DSA_DIM_V + (A.interleaved ? 2 * lane + 1 : lane + 32)] = static_cast<uint8_t>(f8(__fdiv_rn(w.y, s)));
+          }
+        }
       }
     }
   }
@@ -289,13 +388,13 @@ cudaError_t launch_latent_append(const __nv_bfloat16* kv, int64_t ld_kv, const _
   A.G = T / fill < 1 ? 1 : (T / fill > MAX_G ? MAX_G : T / fill);
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) + A.G - 1) / A.G);
   if (!scales) {
-    latent_append_kernel<false, 1><<<grid, THREADS, 0, st>>>(A);
+    latent_append_kernel<false, 1><<<grid, 256, 0, st>>>(A);
   } else {
     // rows a run can have: a warp takes short runs alone
     const int per_seq = (T + B - 1) / B;
     const int rows = per_seq < scale_block ? per_seq : scale_block;
-    if (rows <= 4) latent_append_kernel<true, 1><<<grid, THREADS, 0, st>>>(A);
-    else latent_append_kernel<true, 8><<<grid, THREADS, 0, st>>>(A);
+    if (rows <= 4) latent_append_kernel<true, 1><<<grid, 256, 0, st>>>(A);
+    else latent_append_kernel<true, 16><<<grid, 512, 0, st>>>(A);
   }
   return cudaGetLastError();
 }
