@@ -1167,53 +1167,86 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
 // the first part of query desc[2p + 1] in part 2p + 1, the pairs after it the
 // others in parts 2(p + i), where desc[2(p + i)] is that query again.
 //   LSE = ln sum_i exp(LSE_i),  O = sum_i exp(LSE_i - LSE) O_i.
-// The parts lie as [dim / 4][head][4 dims].  grid (pairs, H / 32, 8): 32 heads,
-// a lane each, and 64 dims a CTA, 8 a warp; the result turns in shared memory.
-constexpr int MT = 256;
-__global__ void __launch_bounds__(MT) attend_merge_kernel(const int32_t* desc, const float* o_part,
-                                                          const float* l_part, int H, __nv_bfloat16* out,
-                                                          float* lse) {
-  __shared__ uint4 turn[32][9];
+// The parts lie as [dim / 4][head][4 dims].  grid (pairs, H / 32, 4): 32 heads,
+// a lane each, and 128 dims a CTA, 16 a warp; the result turns in shared memory.
+// Most CTAs find nothing to merge, so there are few of them; loads of several
+// parts go out together, whether there are that many or not.
+constexpr int MT = 256, MAX_PAIRS = 74;
+__global__ void __launch_bounds__(MT, 4) attend_merge_kernel(const int32_t* desc, const float* o_part,
+                                                             const float* l_part, int H, __nv_bfloat16* out,
+                                                             float* lse) {
+  __shared__ uint4 turn[32][17];
+  __shared__ int tails[MAX_PAIRS];
   pdl_wait();
   const int p = blockIdx.x, pairs = gridDim.x;
   const int q = desc[2 * p + 1];
   if (q < 0) return;
-  int n = 1;
-  while (p + n < pairs && desc[2 * (p + n)] == q) ++n;
+  if (threadIdx.x < pairs) tails[threadIdx.x] = desc[2 * threadIdx.x];
+  __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int h = blockIdx.y * 32 + lane, d4 = blockIdx.z * 16 + 2 * warp;
-  float m = -INFINITY;
-  for (int i = 0; i < n; ++i) m = fmaxf(m, l_part[static_cast<size_t>(2 * (p + i) + (i == 0)) * H + h]);
-  float acc[8] = {};
-  float tot = 0.f;
-  const float m_eff = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const size_t part = 2 * (p + i) + (i == 0);
-    const float w = expf(l_part[part * H + h] - m_eff);
-    const float4* src = reinterpret_cast<const float4*>(o_part) + (part * (DSA_DIM_V / 4) + d4) * H + h;
-    const float4 a = src[0], b = src[H];
-    tot += w;
-    acc[0] = fmaf(w, a.x, acc[0]);
-    acc[1] = fmaf(w, a.y, acc[1]);
-    acc[2] = fmaf(w, a.z, acc[2]);
-    acc[3] = fmaf(w, a.w, acc[3]);
-    acc[4] = fmaf(w, b.x, acc[4]);
-    acc[5] = fmaf(w, b.y, acc[5]);
-    acc[6] = fmaf(w, b.z, acc[6]);
-    acc[7] = fmaf(w, b.w, acc[7]);
+  int n = 1;                                         // parts: this pair's and those of the pairs after it
+  for (uint32_t more = 1; more;) {
+    const int i = p + n + lane;
+    const uint32_t other = __ballot_sync(0xffffffffu, i >= pairs || tails[i] != q);
+    n += other ? __ffs(other) - 1 : 32;
+    more = other == 0;
   }
-  const float inv = tot == 0.f ? 0.f : 1.f / tot;
-  turn[lane][warp] = make_uint4(bf16x2_bits(acc[0] * inv, acc[1] * inv), bf16x2_bits(acc[2] * inv, acc[3] * inv),
-                                bf16x2_bits(acc[4] * inv, acc[5] * inv), bf16x2_bits(acc[6] * inv, acc[7] * inv));
+  const int h = blockIdx.y * 32 + lane;
+  constexpr int UL = 8, U = 4;
+  auto part = [&](int i) { return static_cast<size_t>(2 * (p + i) + (i == 0)); };
+  float m = -INFINITY;
+  for (int i = 0; i < n; i += UL) {
+    float l[UL];
+#pragma unroll
+    for (int k = 0; k < UL; ++k) l[k] = i + k < n ? l_part[part(i + k) * H + h] : -INFINITY;
+#pragma unroll
+    for (int k = 0; k < UL; ++k) m = fmaxf(m, l[k]);
+  }
+  const float m_eff = m == -INFINITY ? 0.f : m;
+  float tot = 0.f;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int d4 = blockIdx.z * 32 + 4 * warp + 2 * t;
+    float acc[8] = {};
+    tot = 0.f;
+    for (int i = 0; i < n; i += U) {
+      float l[U];
+      float4 a[U], b[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const bool is = i + k < n;
+        const float4* src = reinterpret_cast<const float4*>(o_part) + (part(i + k) * (DSA_DIM_V / 4) + d4) * H + h;
+        l[k] = is ? l_part[part(i + k) * H + h] : -INFINITY;
+        a[k] = is ? src[0] : make_float4(0.f, 0.f, 0.f, 0.f);
+        b[k] = is ? src[H] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const float w = expf(l[k] - m_eff);
+        tot += w;
+        acc[0] = fmaf(w, a[k].x, acc[0]);
+        acc[1] = fmaf(w, a[k].y, acc[1]);
+        acc[2] = fmaf(w, a[k].z, acc[2]);
+        acc[3] = fmaf(w, a[k].w, acc[3]);
+        acc[4] = fmaf(w, b[k].x, acc[4]);
+        acc[5] = fmaf(w, b[k].y, acc[5]);
+        acc[6] = fmaf(w, b[k].z, acc[6]);
+        acc[7] = fmaf(w, b[k].w, acc[7]);
+      }
+    }
+    const float inv = tot == 0.f ? 0.f : 1.f / tot;
+    turn[lane][2 * warp + t] =
+        make_uint4(bf16x2_bits(acc[0] * inv, acc[1] * inv), bf16x2_bits(acc[2] * inv, acc[3] * inv),
+                   bf16x2_bits(acc[4] * inv, acc[5] * inv), bf16x2_bits(acc[6] * inv, acc[7] * inv));
+  }
   if (blockIdx.z == 0 && warp == 0) lse[static_cast<size_t>(q) * H + h] = tot == 0.f ? -INFINITY : m_eff + logf(tot);
   __syncthreads();
   const int r = threadIdx.x >> 3, c = threadIdx.x & 7;
-  reinterpret_cast<uint4*>(out + (static_cast<size_t>(q) * H + blockIdx.y * 32 + r) * DSA_DIM_V + 64 * blockIdx.z)[c] =
-      turn[r][c];
+  uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<size_t>(q) * H + blockIdx.y * 32 + r) * DSA_DIM_V + 128 * blockIdx.z);
+  dst[c] = turn[r][c];
+  dst[c + 8] = turn[r][c + 8];
 }
 
-constexpr int MAX_PAIRS = 74;
 constexpr size_t DESC_OFF = 256;
 constexpr size_t L_OFF = DESC_OFF + 2 * MAX_PAIRS * 4 + 176;      // 1024
 static_assert(L_OFF % 256 == 0, "aligned");
@@ -1302,7 +1335,7 @@ cudaError_t launch_attend(const __nv_bfloat16* q, const void* pool, const float*
                       : (kv_scales ? launch<true, false>(a, m, pairs, st) : launch<false, false>(a, m, pairs, st));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(H / 32), DSA_DIM_V / 64);
+  cfg.gridDim = dim3(static_cast<unsigned>(pairs), static_cast<unsigned>(H / 32), DSA_DIM_V / 128);
   cfg.blockDim = dim3(MT, 1, 1);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
