@@ -1008,10 +1008,11 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // NaN stays NaN
       const bool none = l == 0.f;
       // A part goes out as [dim / 4][head][4 dims], so that the lanes of a warp
-      // write next to one another; a result by way of this warp's eighth of P,
-      // 64 bytes of eight heads a store.
+      // write next to one another; a result by way of half of its rows of P (the
+      // four warps of the same rows meet again before one writes P there), 64
+      // bytes of eight heads a store.
       const int d0 = 256 * hh + 128 * cg;
-      uint8_t* stage = ps + (warp - SMX0) * 2048;
+      uint8_t* stage = ps + hh * CH + (quarter & 1) * 4096 + cg * 2048;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         float o[32];
