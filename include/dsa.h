@@ -308,7 +308,7 @@ dsa_status dsa_sparse_mla_decode_fp8(const void* q, const void* kv_pool, float k
  *   k_pe       bf16 [T,64], rows ld_pe elements apart (ld_pe >= 64, even;
  *              4-byte aligned): the RoPE parts before rotation
  *   inv_freq   fp32 [32]: angle of pair i = position * inv_freq[i], reduced
- *              in 64 bits, so far positions keep their angle
+ *              as a 64-bit fraction of a turn, so far positions keep their angle
  *   interleaved  0: pairs (i, i + 32); else pairs (2i, 2i + 1).  A pair (x, y)
  *              becomes (x cos - y sin, y cos + x sin)
  *   kv_pool    the cache, page_table as in dsa_sparse_mla_decode:
@@ -369,8 +369,12 @@ size_t dsa_attend_workspace_bytes(int heads);
  * Precision: products accumulate in fp32 on the tensor cores; scores, maxima
  * and sums are fp32.  Over a bf16 cache the softmax weights are rounded to
  * bf16 for the value product; over an e4m3 cache weights, codes and queries
- * are fp16 there (codes exactly; queries after scaling each head by a power of
+ * are fp16 there (codes exactly; weights times their block's scale, so that
+ * the largest of a head is at least 1 over the largest scale's block, and one
+ * 2^-14 of that has still 11 bits; queries after scaling each head by a power of
  * two, exact except for elements 2^-28 times smaller than the head's largest).
+ * Rows that no sequence holds (before q_offsets[0], from q_offsets[B] on) are
+ * left as they were, whatever their q_vis.
  * ws: at least dsa_attend_workspace_bytes(heads) bytes, 16-byte aligned.
  */
 dsa_status dsa_mla_decode_sinks(const void* q, const void* kv_pool, const float* kv_scales,

@@ -14,45 +14,62 @@
 // nor P cross between the CTAs:
 //   scores  D[64 heads x 128 tokens] a CTA: 36 steps of N = 128
 //   values  D[64 heads x 512 dims]   a CTA: 8 steps of 2 x N = 256
-// 1152 + 1024 tensor cycles a tile, the count of the formula.  Shared memory
-// is read and written at about 120 of its 128 bytes a cycle meanwhile, so a
-// smaller tile, which re-reads the query more often, would be bound by it.
-// With two accumulator halves in the lanes, a head's row of scores lies in two
-// threads (tokens 0..63 and 64..127), which exchange their maxima.
+// About 2200 tensor cycles a tile.  A CTA alone would have to hold the query of
+// all heads (144 KB), or read every token for each half of them.
 //
 // The work is cut evenly: the tiles of all queries, one after another, are
-// divided over the SM pairs, so ragged lists leave no pair idle; a query whose
-// tiles lie on several pairs leaves partial results that a second kernel
-// merges by log-sum-exp.
+// divided over the SM pairs, so ragged lists leave no pair idle; where there are
+// enough of them a query counts START tiles more, what beginning one costs.  A
+// query whose tiles lie on several pairs leaves partial results that a second
+// kernel merges by log-sum-exp.
 //
 // Operands.  bf16 cache: q, C and P as bf16 (P's rounding, 2^-9 of each
 // weight, is the size of the output's own).  e4m3 cache: codes widened to fp16
 // (exact), q scaled by a power of two a head so that its largest element lies
 // in [2^14, 2^15) and rounded to fp16 (exact for all that is not 2^-28 times
-// smaller), P as fp16.  The scales enter in fp32: z_j takes s_j, and P_j is
-// formed as exp2(z_j + log2 s_j - m) with m the running maximum of that sum,
-// so that P <= 2^8 whatever the scales are; l sums exp2(z_j - m).  Sums, maxima
-// and O are fp32.
+// smaller), P as fp16.  The scales enter in fp32.  A tile whose scales lie within
+// a factor of 2^15 has one, its largest s, and its tokens factors f_j = s_j / s:
+// with z_j = q . code_j f_j s + log2 s, P_j = exp2(z_j - m) f_j <= 2^8 and
+// l = sum exp2(z_j - m) / s.  Another tile takes s_j for s and f_j = 1.  m is
+// the running maximum of z, log2 s included, so that P fits whatever the scales
+// are; P's smallest normal value is 2^-14, and down to there it keeps 11 bits.
+// Sums, maxima and O are fp32.
 //
 // Tensor memory (512 columns): O [0,256), lanes 0..63 dims 0..255 of the CTA's
 // heads, lanes 64..127 dims 256..511 | scores slot 0 [256,320) | slot 1
-// [320,384).  Shared memory: the query (72 KB), P (16 KB), keys as a ring of
-// chunks (64 tokens x 64 dims), values as a ring of slots (16 tokens x 256
-// dims, one MMA step), refilled as soon as their MMAs have read them; all in the
-// 128-byte swizzle.  A bf16 cache's rings hold a whole tile and are filled by
-// gathering TMA loads of four rows.  An e4m3 cache has a tile's codes gathered
-// the same way and widened into shorter rings by eight warps.  TMA carries
-// all gathers: the same loads issued by threads (cp.async, or registers) fill the
-// load/store unit's queue, behind which every barrier and fence of the SM waits;
-// a tile took 10,500 cycles that way, three times its MMAs.
+// [320,384).  Shared memory: the query (72 KB), P (16 KB), the rings of keys and
+// values in the 128-byte swizzle, refilled as soon as their MMAs have read them:
+//   bf16   keys three groups of 3 chunks (64 tokens x 64 dims), values three
+//          units of 32 tokens x 256 dims, all filled by TMA
+//   e4m3   raw units by TMA (keys 64 tokens x 256 codes twice and the positions,
+//          values 2 x 32 tokens x 256 codes) and widened into two slots of 2
+//          chunks, one of the positions, and two value units
+// A load costs about 45 cycles to issue whatever it brings (a gather of four rows
+// 57), so 16 rows that are consecutive in the pool come as one box (of the bf16
+// keys 8), others by gathers of four.  Rows that the list does not hold are
+// loaded from outside the pool, as zeros, and never read, so that what lies in
+// the cache there (NaN, say) cannot reach a product.  TMA carries all of it: the
+// same loads issued by threads (cp.async, or registers) fill the load/store
+// unit's queue, behind which every barrier and fence of the SM waits; a tile
+// took 10,500 cycles that way.
 //
 // Roles: warp 0 of the first CTA issues the MMAs of both; warp 1 loads queries
 // and keys, warp 2 values; warp 3 looks up pool rows (list -> page table ->
-// scale), the loads of three tiles under way at once; warps 4..7 softmax,
-// rescale and output, half a head a thread; for an e4m3 cache warps 8..11 widen
-// keys and scale the query, warps 12..15 widen values.  Rows that the list does
-// not hold are gathered from outside the pool, as zeros, and never read, so that
-// what lies in the cache there (NaN, say) cannot reach a product.
+// scale), the loads of three tiles under way at once, and sends the rows to L2;
+// warps 4..11 softmax, rescale and output, a row's 128 tokens and 512 dims in four
+// parts, one a thread, which exchange their maxima; for an e4m3 cache warps
+// 12..15 widen keys and scale the query, warps 16..19 widen values.
+//
+// What bounds it.  bf16: a tile takes about 4900 cycles on a pair, its 147 KB from
+// DRAM at a 74th of the copy rate 3100; the rings, all the shared memory there
+// is, hold one tile, so a load's latency is not quite covered.  16 users, 128 heads,
+// windows of 8192: 57.8 us, 2.3 TB/s.  e4m3: about 7000 cycles, of which the MMAs
+// are 2200: the widening reads 1 and writes 2 bytes a code to shared memory, beside
+// the 4 that MMAs read for it, and its issue slots are shared with the softmax.
+// 4 users, 128 heads, dense over 131072 tokens: 214 us, 682 TFLOP/s, 1.4 TB/s of
+// codes.  About 15 us of a launch are not tiles: the shares, the first look-up
+// (three dependent loads), cold instructions (the hot code is kept below 60 KB:
+// past the instruction cache every warp slows down several times), output, merge.
 #include "common.cuh"
 #include "internal.h"
 
@@ -161,8 +178,15 @@ struct List {
   }
 };
 
+// whether a sequence holds query q; the results of others stay as they were
+__device__ __forceinline__ bool held(const AttendArgs& a, int q) {
+  const int first = __ldg(a.q_offsets), end = __ldg(a.q_offsets + a.B);
+  return (q >= first) & (q < end);
+}
+
 __device__ __forceinline__ int visible(const AttendArgs& a, int q) {
-  const int v = max(0, __ldg(a.q_vis + q));
+  const int seen = __ldg(a.q_vis + q);               // in flight beside the offsets
+  const int v = held(a, q) ? max(0, seen) : 0;
   const int64_t cap = static_cast<int64_t>(a.max_pages) << a.page_shift;
   return v < cap ? v : static_cast<int>(cap);
 }
@@ -266,8 +290,9 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 }
 
 // Arrive on a barrier of the cluster (its address there) after this CTA's own
-// shared-memory writes, which the fence before has made the tensor core's: the
-// release at cluster scope of mbar_arrive_remote waits for every access under way
+// shared-memory writes, which the fence before has made the tensor core's.  At
+// the default scope: a release at cluster scope (mbar_arrive_remote) waits for
+// every access under way, 1300 to 2000 cycles here
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -832,7 +857,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         at[k] = pos[k] >= 0 && pos[k] < vis1 ? pos[k] : -1;
-        bad |= at[k] != pos[k] && pos[k] != -1;
+        bad |= at[k] != pos[k] && pos[k] != -1 && vis1 >= 0;
         pg[k] = at[k] >= 0 ? __ldg(pages1 + (at[k] >> a.page_shift)) : -1;
       }
       if (i < ntile && u == n) {
@@ -843,8 +868,9 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         u = 0;
         pages = a.page_table + static_cast<size_t>(seq_of_query(a.q_offsets, a.B, q, lane)) * a.max_pages;
         vis = visible(a, q);
-        bad |= __ldg(a.q_vis + q) > vis;
         ls = list_of(a, vis);
+        if (!held(a, q)) vis = -1;                   // nothing is read, and no index is a fault
+        else bad |= __ldg(a.q_vis + q) > vis;
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -1004,7 +1030,8 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       const bool whole = n == nt;
       const bool head = off == 0;
       const int part = 2 * pair + (head ? 1 : 0);
-      if (!whole) (head ? head_q : tail_q) = q;
+      const bool mine = held(a, q);
+      if (!whole && mine) (head ? head_q : tail_q) = q;
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // NaN stays NaN
       const bool none = l == 0.f;
       // A part goes out as [dim / 4][head][4 dims], so that the lanes of a warp
@@ -1033,7 +1060,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
             const int hr = 8 * i + (lane >> 2);
             const uint4 w = lds16(stage + hr * 64 + ((piece ^ (hr >> 1 & 3)) << 4));
             const size_t row = static_cast<size_t>(q) * a.H + half * HC + (quarter & 1) * 32 + hr;
-            *reinterpret_cast<uint4*>(a.out + row * DSA_DIM_V + d0 + 32 * c + 8 * piece) = w;
+            if (mine) *reinterpret_cast<uint4*>(a.out + row * DSA_DIM_V + d0 + 32 * c + 8 * piece) = w;
           }
           __syncwarp();
         } else {
@@ -1043,7 +1070,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
           for (int i = 0; i < 8; ++i) dst[i * a.H] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         }
       }
-      if (hh == 0 && cg == 0)
+      if (hh == 0 && cg == 0 && mine)
         (whole ? a.lse + static_cast<size_t>(q) * a.H + h : a.l_part + static_cast<size_t>(part) * a.H + h)[0] =
             none ? -INFINITY : (m_use + log2f(l)) * 0.69314718055994531f;
       tc_fence_before();                             // O was read before the next segment writes it
@@ -1170,8 +1197,10 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
 //   LSE = ln sum_i exp(LSE_i),  O = sum_i exp(LSE_i - LSE) O_i.
 // The parts lie as [dim / 4][head][4 dims].  grid (pairs, H / 32, 4): 32 heads,
 // a lane each, and 128 dims a CTA, 16 a warp; the result turns in shared memory.
-// Most CTAs find nothing to merge, so there are few of them; loads of several
-// parts go out together, whether there are that many or not.
+// Bound by latency: the loads of several parts go out together, whether there are
+// that many or not (one user's step over 2048 selected tokens 28.7 -> 27.4 us).
+// Most CTAs find nothing to merge and end; a grid that is resident at once and
+// shares out what there is took 5 us more.
 constexpr int MT = 256, MAX_PAIRS = 74;
 __global__ void __launch_bounds__(MT, 4) attend_merge_kernel(const int32_t* desc, const float* o_part,
                                                              const float* l_part, int H, __nv_bfloat16* out,
