@@ -41,35 +41,43 @@
 // values in the 128-byte swizzle, refilled as soon as their MMAs have read them:
 //   bf16   keys three groups of 3 chunks (64 tokens x 64 dims), values three
 //          units of 32 tokens x 256 dims, all filled by TMA
-//   e4m3   raw units by TMA (keys 64 tokens x 256 codes twice and the positions,
-//          values 2 x 32 tokens x 256 codes) and widened into two slots of 2
-//          chunks, one of the positions, and two value units
+//   e4m3   raw units by TMA (keys 64 tokens x 256 and x 320 codes, values 2 x 32
+//          tokens x 256 codes), widened into two slots of 2 chunks, one of the
+//          positions, and two value units
 // A load costs about 45 cycles to issue whatever it brings (a gather of four rows
 // 57), so 16 rows that are consecutive in the pool come as one box (of the bf16
 // keys 8), others by gathers of four.  Rows that the list does not hold are
 // loaded from outside the pool, as zeros, and never read, so that what lies in
-// the cache there (NaN, say) cannot reach a product.  TMA carries all of it: the
-// same loads issued by threads (cp.async, or registers) fill the load/store
-// unit's queue, behind which every barrier and fence of the SM waits; a tile
-// took 10,500 cycles that way.
+// the cache there (NaN, say) cannot reach a product.  For the same reason two
+// queries of 64 heads do not share a tile: a token that one of them lists would
+// meet the other's zero weight.  TMA carries all of it: the same loads issued by
+// threads (cp.async, or registers) fill the load/store unit's queue, behind which
+// every barrier and fence of the SM waits; a tile took 10,500 cycles that way.
 //
-// Roles: warp 0 of the first CTA issues the MMAs of both; warp 1 loads queries
-// and keys, warp 2 values; warp 3 looks up pool rows (list -> page table ->
-// scale), the loads of three tiles under way at once, and sends the rows to L2;
-// warps 4..11 softmax, rescale and output, a row's 128 tokens and 512 dims in four
-// parts, one a thread, which exchange their maxima; for an e4m3 cache warps
-// 12..15 widen keys and scale the query, warps 16..19 widen values.
+// Roles, by warp:
+//   0       score MMAs of both CTAs (in the first)      1  loads queries and keys
+//   2       loads values      3  looks up pool rows (list -> page table -> scale),
+//           the loads of three tiles under way at once, and sends the rows to L2
+//   4..11   softmax, rescale and output, a row's 128 tokens and 512 dims in four
+//           parts, one a thread, which exchange their maxima
+//   bf16: 12 value MMAs; e4m3: 12..19 widen keys and scale the query, 20..23 widen
+//   values, 24 value MMAs
+// The two sorts of MMAs have a warp each, since waiting and issuing take longer
+// than the MMAs themselves (one warp for both: 24 verifying users 47.4 against
+// 45.1 us), and so that scores run up to two tiles ahead.  Widening the keys was the
+// longest chain, so two groups of four warps take turns at it (32 users, windows of
+// 4096: 72.6 -> 69.5 us).
 //
-// What bounds it.  bf16: a tile takes about 4900 cycles on a pair, its 147 KB from
+// What bounds it.  bf16: a tile takes about 4200 cycles on a pair, its 147 KB from
 // DRAM at a 74th of the copy rate 3100; the rings, all the shared memory there
 // is, hold one tile, so a load's latency is not quite covered.  16 users, 128 heads,
-// windows of 8192: 57.8 us, 2.3 TB/s.  e4m3: about 7000 cycles, of which the MMAs
-// are 2200: the widening reads 1 and writes 2 bytes a code to shared memory, beside
-// the 4 that MMAs read for it, and its issue slots are shared with the softmax.
-// 4 users, 128 heads, dense over 131072 tokens: 214 us, 682 TFLOP/s, 1.4 TB/s of
-// codes.  About 15 us of a launch are not tiles: the shares, the first look-up
-// (three dependent loads), cold instructions (the hot code is kept below 60 KB:
-// past the instruction cache every warp slows down several times), output, merge.
+// windows of 8192: 57.6 us, 2.3 TB/s.  e4m3: about 5300 cycles, of which the MMAs
+// are 2200; shared memory moves some 4000 cycles' worth a tile (the widening reads 1 and
+// writes 2 bytes a code, MMAs read 4 for it), the softmax is busy for 3600.  4 users,
+// 128 heads, dense over 131072 tokens: 211 us, 691 TFLOP/s, 1.4 TB/s of codes.
+// About 15 us of a launch are not tiles: the shares, the first look-up (three
+// dependent loads), cold instructions (the hot code is kept below 60 KB: past the
+// instruction cache every warp slows down several times), output, merge.
 #include "common.cuh"
 #include "internal.h"
 
@@ -89,20 +97,21 @@ constexpr int VCH = 16 * 128;                        // bytes of 16 tokens x 64 
 constexpr int VSTEP = 4 * VCH;                       // and x 256 dims: one MMA step
 constexpr int VSLOT = VT / 16 * VSTEP;
 constexpr int VS = NT / VT;                          // units a tile takes
-constexpr int KU = 3;                                // units of a tile's key codes: 2 of 256 dims, the positions
-constexpr int KUB = NH * 256;                        // bytes of a wide unit
+constexpr int KU = 2;                                // units of a tile's key codes: 256 dims, 320 dims
+constexpr int KUB = NH * 256;                        // bytes of the first
 constexpr int VUB = VT * 256;                        // bytes of a value unit's codes
 constexpr int VUR = 2;                               // units of their ring
 constexpr int RUN = 16;                              // rows that one load can bring where they are consecutive
 constexpr int START = 2;                              // tiles that beginning a query costs
-constexpr int RR = 3;                                // tiles looked up ahead
+constexpr int RR = 4;                                // tiles looked up ahead
+constexpr int QM = 4;                                // queries whose factors are kept
 constexpr int SMX = 8;                               // softmax warps
 constexpr int GROUP = 4;                             // warps that widen keys; as many widen values
 constexpr int SMX0 = 4;                              // first of the softmax warps
 
 template <bool KV8>
 struct Plan {
-  static constexpr int WARPS = SMX0 + SMX + (KV8 ? 2 * GROUP : 0);
+  static constexpr int WARPS = SMX0 + SMX + (KV8 ? 4 * GROUP : 1);
   static constexpr int THREADS = 32 * WARPS;
   // A tile's 9 key chunks come in groups, each with its slot: three of three, or
   // (e4m3) four of two, through two slots, and the positions.
@@ -115,21 +124,21 @@ struct Plan {
   static constexpr int OFF_V = OFF_K + (KV8 ? 5 : 9) * CH;
   static constexpr int OFF_P = OFF_V + VR * VSLOT;   // [2][64 heads x 64 tokens]
   static constexpr int OFF_KU = OFF_P + 2 * CH;      // e4m3: units of a tile's keys
-  static constexpr int OFF_VU = OFF_KU + (KV8 ? 2 * KUB + NH * 64 : 0);
+  static constexpr int OFF_VU = OFF_KU + (KV8 ? NH * DSA_DIM : 0);
   static constexpr int OFF_SCL = OFF_VU + (KV8 ? VUR * VUB : 0);       // e4m3: float [RR][128]: scale of each token, over the tile's where it has one
   static constexpr int OFF_TILE = OFF_SCL + (KV8 ? RR * NT * 4 : 0);  // float4 [RR]: scale, log2, 1 / scale of the tile; w: it has one
   static constexpr int OFF_ROWS = OFF_TILE + (KV8 ? RR * 16 : 0);      // int32 [RR][128]: pool row or -1
   static constexpr int OFF_MASK = OFF_ROWS + RR * NT * 4;            // uint32 [RR][4]: tokens that count
   static constexpr int OFF_RUNS = OFF_MASK + RR * 4 * 4;             // uint32 [4]: bit i: rows 16 i .. 16 i + 15 are consecutive, or none is held
-  static constexpr int OFF_QMUL = OFF_RUNS + 16;                     // float [2][64], by segment
-  static constexpr int OFF_MX = OFF_QMUL + 2 * RH * 4;               // float [2][4][64]: between the parts of a row
-  static constexpr int OFF_SCAN = OFF_MX + 8 * RH * 4;               // int64 [20]; the share's first and last tile; its first query and that one's tile
-  static constexpr int OFF_BAR = OFF_SCAN + 24 * 8;
-  static constexpr int NBAR = 2 * RR + 2 * KS + 2 * VR + 2 + 4 + (KV8 ? 1 + 2 * KU + 2 * VUR : 0);
+  static constexpr int OFF_QMUL = OFF_RUNS + 16;                     // float [QM][64], by segment
+  static constexpr int OFF_MX = OFF_QMUL + QM * RH * 4;              // float [2][4][64]: between the parts of a row
+  static constexpr int OFF_SCAN = OFF_MX + 8 * RH * 4;               // int64 [28]; the share's first and last tile; its first query and that one's tile
+  static constexpr int OFF_BAR = OFF_SCAN + 32 * 8;
+  static constexpr int NBAR = 2 * RR + 2 * KS + 2 * VR + 4 + 4 + (KV8 ? 1 + 2 * KU + 2 * VUR : 0);
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 16;
   static_assert(SMEM_BYTES <= 232448, "shared memory exceeds the sm_100 limit");
-  static_assert(WARPS <= 20, "scan");
+  static_assert(WARPS <= 28, "scan");
 };
 constexpr uint32_t O_COL = 0, S_COL = 256, TMEM_COLS = 512;
 
@@ -157,8 +166,8 @@ struct AttendMaps {
   CUtensorMap q;                                     // [Q * H][576], boxes of 64 dims x a CTA's heads
   CUtensorMap row;                                   // 64 dims (bf16) or 256 codes
   CUtensorMap run;                                   // bf16: 8 rows x 3 chunks of 64 dims; e4m3: 16 rows x 256 codes
-  CUtensorMap row_pos;                               // e4m3: 64 codes
-  CUtensorMap run_pos;                               // bf16: 16 rows x 4 chunks; e4m3: 16 rows x 64 codes
+  CUtensorMap row_hi;                                // e4m3: 320 codes, in words of four
+  CUtensorMap run_hi;                                // bf16: 16 rows x 4 chunks; e4m3: 16 rows x 320 codes
 };
 
 // The list of a query with `vis` visible tokens, laid out in entries: the
@@ -375,8 +384,8 @@ __device__ __forceinline__ void store_wide(uint8_t* dst, int p, int sw, int flip
 }
 
 // The query as fp16 in place, each head scaled so that its largest element lies
-// in [2^14, 2^15); infinities and NaN stay what they are.  A warp takes a
-// quarter of the heads, two at a time; 72 pieces of 8 dims a head.  A function of
+// in [2^14, 2^15); infinities and NaN stay what they are.  A warp takes
+// an eighth of the heads, two at a time; 72 pieces of 8 dims a head.  A function of
 // its own, since two places call it.
 __device__ __noinline__ void scale_query(uint8_t* qs, float* qmul, int heads, int lw, int lane) {
 #pragma unroll 1
@@ -441,12 +450,13 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   uint64_t* v_full = k_empty + KS;         // [VR]
   uint64_t* v_empty = v_full + VR;
   uint64_t* s_full = v_empty + VR;         // [2] scores of a tile are in their slot
-  uint64_t* p_full = s_full + 2;           // P of a tile is in shared memory
+  uint64_t* s_empty = s_full + 2;          // [2] they are read
+  uint64_t* p_full = s_empty + 2;          // P of a tile is in shared memory
   uint64_t* pv_done = p_full + 1;          // its value MMAs are done: P is free, O holds
   uint64_t* q_full = pv_done + 1;          // a segment's query is in shared memory
   uint64_t* q_empty = q_full + 1;          // its scores are done
   uint64_t* q_raw = q_empty + 1;           // e4m3: this CTA's part as bf16
-  uint64_t* ku_full = q_raw + 1;           // e4m3: [3] units of key codes
+  uint64_t* ku_full = q_raw + 1;           // e4m3: [2] units of key codes
   uint64_t* ku_empty = ku_full + KU;
   uint64_t* vu_full = ku_empty + KU;       // e4m3: [2] units of value codes
   uint64_t* vu_empty = vu_full + VUR;
@@ -462,8 +472,8 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     tma_prefetch_desc(&maps.row);
     tma_prefetch_desc(&maps.run);
     if (KV8) {
-      tma_prefetch_desc(&maps.row_pos);
-      tma_prefetch_desc(&maps.run_pos);
+      tma_prefetch_desc(&maps.row_hi);
+      tma_prefetch_desc(&maps.run_hi);
     }
   }
 
@@ -473,11 +483,12 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     const int full = KV8 ? 2 * GROUP : 1;            // widened operands: a warp each
     int n = 1;
     if (i >= RR && i < 2 * RR) n = 2 + live_smx;
-    if (i >= k_full - bars && i < k_empty - bars) n = full;
+    if (i >= k_full - bars && i < k_empty - bars) n = KV8 ? 2 * GROUP : 1;
     if (i >= v_full - bars && i < v_empty - bars) n = full;
-    if (i == p_full - bars) n = 2 * live_smx;
-    if (i == q_full - bars) n = full;
-    if (KV8 && ((i >= ku_empty - bars && i < vu_full - bars) || i >= vu_empty - bars)) n = GROUP;
+    if (i >= s_empty - bars && i <= p_full - bars) n = 2 * live_smx;
+    if (i == q_full - bars) n = KV8 ? 4 * GROUP : 1;
+    if (KV8 && i >= ku_empty - bars && i < vu_full - bars) n = 2 * GROUP;
+    if (KV8 && i >= vu_empty - bars) n = GROUP;
     mbar_init(bars + i, n);
     mbar_fence_init();
   }
@@ -498,7 +509,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     if (lane >= o) incl += v;
   }
   if (lane == 31) scan[warp] = incl;
-  if (tid < 2) scan[20 + tid] = 0;
+  if (tid < 2) scan[28 + tid] = 0;
   __syncthreads();
   int64_t base = 0, total = 0;
 #pragma unroll 1
@@ -518,7 +529,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     const uint32_t p = min(pair + i, np);
     const int64_t c = p == np ? cost : each * p + min(p, over);
     if (p == np) {
-      if (tid == 0) scan[20 + i] = total;
+      if (tid == 0) scan[28 + i] = total;
     } else {
       int64_t at = base;
       const int64_t at_cost = base + static_cast<int64_t>(start) * qa;
@@ -531,10 +542,10 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
           at += n;
         }
         const int64_t off = left > start ? left - start : 0;
-        scan[20 + i] = at + off;
+        scan[28 + i] = at + off;
         if (i == 0) {
-          scan[22] = q;
-          scan[23] = off;
+          scan[30] = q;
+          scan[31] = off;
         }
       }
     }
@@ -543,9 +554,9 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   cluster_sync();                                    // both CTAs' barriers and tensor memory are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  const int q0 = static_cast<int>(scan[22]);
-  const int off0 = static_cast<int>(scan[23]);
-  const int ntile = static_cast<int>(scan[21] - scan[20]);
+  const int q0 = static_cast<int>(scan[30]);
+  const int off0 = static_cast<int>(scan[31]);
+  const int ntile = static_cast<int>(scan[29] - scan[28]);
   if (half == 0 && tid < 2 && ntile == 0) a.desc[2 * pair + tid] = -1;
 
   // the first CTA's barrier of the same name
@@ -577,83 +588,48 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   };
 
   if (warp == 0) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ score MMAs
     // The warp walks together, so that descriptors stay in uniform registers,
     // and one elected lane issues.
     constexpr uint32_t fmt = KV8 ? 0u /*F16*/ : 1u /*BF16*/;
     constexpr uint32_t idesc_s = umma_idesc(fmt, 128, NT);
-    constexpr uint32_t idesc_pv = umma_idesc(fmt, 128, 256, 0, 1);
     const uint64_t dq = umma_desc_sw128(smem_u32(qs), 1024, 16);
     const uint64_t dk = umma_desc_sw128(smem_u32(ks), KV8 ? 1024 : 1024 * KCH, 16);
-    const uint64_t dp = umma_desc_sw128(smem_u32(ps), 1024, 16);
-    const uint64_t dv = umma_desc_sw128_mn(smem_u32(vs), VCH, 1024);
     const bool lead = elect_one();
     bool ok = true;
     int q = q0, off = off0, left = half == 0 ? ntile : 0;
     uint32_t g = 0;                              // tiles so far
-    Ring<VR> vr;
 #pragma unroll 1
     for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
       const int n = min(tiles_of<IDX>(a, q) - off, left);
       left -= n;
       if (!(ok = await(q_full, seg & 1, a.err))) break;
-      // the scores of tile u before the values of tile u - 1, so that the
-      // softmax of each runs beside MMAs
 #pragma unroll 1
-      for (int u = 0; u <= n && ok; ++u) {
-        const uint32_t gu = g + u;
-        if (u < n) {
-          const uint32_t d = tmem + S_COL + (gu & 1) * NH;
+      for (int u = 0; u < n && ok; ++u, ++g) {
+        const uint32_t d = tmem + S_COL + (g & 1) * NH;
+        if (!(ok = await(&s_empty[g & 1], ((g >> 1) & 1) ^ 1, a.err))) break;
 #pragma unroll 1
-          for (int j = 0; j < KG; ++j) {
-            const int slot = key_slot(j), nc = KV8 && j == 4 ? 1 : KCH;
-            if (!(ok = await(&k_full[slot], key_use(j, gu), a.err))) break;
-            tc_fence_after();
-            if (lead) {
-#pragma unroll 1
-              for (int c = 0; c < nc; ++c) {
-                const uint64_t dqc = dq + (KCH * j + c) * (CH >> 4), dkc = dk + (KCH * slot * CH + c * (KV8 ? CH : 1024)) / 16;
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_f16_pair(d, dqc + k * 2, dkc + k * 2, idesc_s, j > 0 || c > 0 || k > 0 ? 1u : 0u);
-              }
-              mma_commit_pair(&k_empty[slot]);
-            }
-            __syncwarp();
-          }
-          if (!ok) break;
+        for (int j = 0; j < KG; ++j) {
+          const int slot = key_slot(j), nc = KV8 && j == 4 ? 1 : KCH;
+          if (!(ok = await(&k_full[slot], key_use(j, g), a.err))) break;
+          tc_fence_after();
           if (lead) {
-            mma_commit_pair(&s_full[gu & 1]);
-            if (u == n - 1) mma_commit_pair(q_empty);
-          }
-          __syncwarp();
-        }
-        if (u >= 1) {
-          if (!(ok = await(p_full, (gu - 1) & 1, a.err))) break;
 #pragma unroll 1
-          for (int i = 0; i < VS; ++i) {
-            if (!(ok = await(&v_full[vr.slot], vr.use, a.err))) break;
-            tc_fence_after();
-            if (lead) {
+            for (int c = 0; c < nc; ++c) {
+              const uint64_t dqc = dq + (KCH * j + c) * (CH >> 4), dkc = dk + (KCH * slot * CH + c * (KV8 ? CH : 1024)) / 16;
 #pragma unroll
-              for (int k = 0; k < VT / 16; ++k) {
-                const uint64_t dpi = dp + (i >> 1) * (CH >> 4) + (i & 1) * 4 + k * 2;
-                const uint64_t dvi = dv + vr.slot * (VSLOT >> 4) + k * (VSTEP >> 4);
-                const uint32_t acc = u > 1 || i > 0 || k > 0 ? 1u : 0u;
-                mma_f16_pair(tmem + O_COL, dpi, dvi, idesc_pv, acc);
-                mma_f16_pair(tmem + O_COL + 128, dpi, dvi + (2 * VCH >> 4), idesc_pv, acc);
-              }
-              mma_commit_pair(&v_empty[vr.slot]);
+              for (int k = 0; k < 4; ++k)
+                mma_f16_pair(d, dqc + k * 2, dkc + k * 2, idesc_s, j > 0 || c > 0 || k > 0 ? 1u : 0u);
             }
-            __syncwarp();
-            vr.next();
+            mma_commit_pair(&k_empty[slot]);
+            if (j == KG - 1) {
+              mma_commit_pair(&s_full[g & 1]);
+              if (u == n - 1) mma_commit_pair(q_empty);
+            }
           }
-          if (!ok) break;
-          if (lead) mma_commit_pair(pv_done);
           __syncwarp();
         }
       }
-      g += n;
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ queries, keys
@@ -680,19 +656,19 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         const int r0 = run_start(static_cast<int>(r.x));
         const int i = lane >> 2, t = lane & 3;
 #pragma unroll 1
-        for (int j = 0; j < 3; ++j) {
+        for (int j = 0; j < (KV8 ? KU : 3); ++j) {
           uint64_t* full = KV8 ? &ku_full[j] : &k_full[j];
           if (!(ok = await(KV8 ? &ku_empty[j] : &k_empty[j], (g & 1) ^ 1, a.err))) break;
           if constexpr (KV8) {
-            const int pitch = j < 2 ? 256 : 64;
+            const int pitch = j == 0 ? 256 : 320;
             uint8_t* dst = smem + L::OFF_KU + j * KUB + lane * 4 * pitch;
             if (lead) mbar_arrive_expect_tx(full, NH * pitch);
             __syncwarp();
             if (lane < 16 && !run)
-              gather4_pair(dst, j < 2 ? &maps.row : &maps.row_pos, 256 * j, r, smem_u32(full));
+              gather4_pair(dst, j == 0 ? &maps.row : &maps.row_hi, 64 * j, r, smem_u32(full));
             __syncwarp();
             if (lane < 16 && run && t == 0)
-              load_2d_pair(dst, j < 2 ? &maps.run : &maps.run_pos, 256 * j, r0, smem_u32(full));
+              load_2d_pair(dst, j == 0 ? &maps.run : &maps.run_hi, 64 * j, r0, smem_u32(full));
           } else {
             const uint32_t bar = leader(full);
             uint8_t* dst = ks + j * KCH * CH + (i * 2 + (t >> 1)) * KCH * 1024 + (t & 1) * 512;
@@ -754,7 +730,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
           __syncwarp();
           if (!run) gather4_pair(dst, &maps.row, 256 * half + 64 * d, r, bar);
           __syncwarp();
-          if (run && (lane & 15) == 0) load_3d_pair(dst, &maps.run_pos, r0, 4 * half, bar);
+          if (run && (lane & 15) == 0) load_3d_pair(dst, &maps.run_hi, r0, 4 * half, bar);
         }
         __syncwarp();
         ur.next();
@@ -894,6 +870,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     // ------------------------------------------------------------ softmax, output
     // thread: accumulator row r, the tile's tokens 64 hh + 32 cg .. + 31, and
     // value dims 256 hh + 128 cg .. + 127; part = 2 hh + cg
+    if constexpr (KV8) asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
     const int quarter = warp & 3, hh = quarter >> 1, cg = (warp - SMX0) >> 2;
     const int r = (quarter & 1) * 32 + lane;
     const int h = half * HC + r;
@@ -919,8 +896,12 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         float z[32];
         tmem_ld32(lane_base + S_COL + sb * NH + cg * 32, z);
         // the scores are there, so the query's factors are
-        if (KV8 && u == 0) qm = qmul[(seg & 1) * RH + r];
+        if (KV8 && u == 0) qm = qmul[(seg % QM) * RH + r];
         tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(leader(&s_empty[sb]));
+        __syncwarp();
         float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
         float4 ts = make_float4(a.scale_log2, 0.f, 1.f, 1.f);
         if constexpr (KV8) ts = tsc[slot];
@@ -1080,24 +1061,68 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       a.desc[2 * pair + 1] = head_q;
     }
     __syncwarp();
-  } else if (KV8 && warp < SMX0 + SMX + GROUP) {
+  } else if (warp >= SMX0 + SMX + (KV8 ? 3 * GROUP : 0)) {
+    // ------------------------------------------------------------ value MMAs
+    // e4m3: the seven warp groups start with 72 registers a thread, of which the
+    // softmax needs more, the widening and this group, one warp of which works, less:
+    // 72 + 2 x 96 + 3 x 64 + 48 = 7 x 72
+    if constexpr (KV8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+    constexpr uint32_t idesc_pv = umma_idesc(KV8 ? 0u : 1u, 128, 256, 0, 1);
+    const uint64_t dp = umma_desc_sw128(smem_u32(ps), 1024, 16);
+    const uint64_t dv = umma_desc_sw128_mn(smem_u32(vs), VCH, 1024);
+    const bool lead = elect_one();
+    bool ok = true;
+    int q = q0, off = off0, left = half == 0 && warp == SMX0 + SMX + (KV8 ? 3 * GROUP : 0) ? ntile : 0;
+    uint32_t g = 0;
+    Ring<VR> vr;
+#pragma unroll 1
+    for (; left > 0 && ok; ++q, off = 0) {
+      const int n = min(tiles_of<IDX>(a, q) - off, left);
+      left -= n;
+#pragma unroll 1
+      for (int u = 0; u < n && ok; ++u, ++g) {
+        if (!(ok = await(p_full, g & 1, a.err))) break;
+#pragma unroll 1
+        for (int i = 0; i < VS; ++i) {
+          if (!(ok = await(&v_full[vr.slot], vr.use, a.err))) break;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int k = 0; k < VT / 16; ++k) {
+              const uint64_t dpi = dp + (i >> 1) * (CH >> 4) + (i & 1) * 4 + k * 2;
+              const uint64_t dvi = dv + vr.slot * (VSLOT >> 4) + k * (VSTEP >> 4);
+              const uint32_t acc = u > 0 || i > 0 || k > 0 ? 1u : 0u;
+              mma_f16_pair(tmem + O_COL, dpi, dvi, idesc_pv, acc);
+              mma_f16_pair(tmem + O_COL + 128, dpi, dvi + (2 * VCH >> 4), idesc_pv, acc);
+            }
+            mma_commit_pair(&v_empty[vr.slot]);
+            if (i == VS - 1) mma_commit_pair(pv_done);
+          }
+          __syncwarp();
+          vr.next();
+        }
+      }
+    }
+  } else if (KV8 && warp < SMX0 + SMX + 2 * GROUP) {
     // ------------------------------------------------------------ e4m3: keys widened, queries scaled
-    // Two chunks at a time.  thread: 16 codes of four tokens; those of the next
-    // chunks come to registers while these are widened.  Lanes of odd chunks store
-    // their two pieces in the other order, so that the eight lanes of a store lie
-    // in different banks.
-    const int lw = warp - (SMX0 + SMX);
-    const int lt = lw * 32 + lane;
+    // Two chunks at a time, the first and third pair of them by one group of four
+    // warps, the second and fourth by another; the positions by the first.  thread:
+    // 16 codes of four tokens; those of the next pair come to registers while these
+    // are widened.  Lanes of odd chunks store their two pieces in the other order,
+    // so that the eight lanes of a store lie in different banks.
+    if constexpr (KV8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    const int lw = warp - (SMX0 + SMX), team = lw / GROUP;
+    const int lt = (lw % GROUP) * 32 + lane;
     const int pc = lt & 7, r0 = lt >> 3, flip = pc >> 2, rp = lt >> 2;
     bool ok = true;
     int off = off0, left = ntile, n = 0, u = 0, q = q0;
     uint32_t seg = 0;
     auto query = [&]() {
       if (!(ok = ok && await(q_raw, seg & 1, a.err))) return;
-      scale_query(qs, qmul + (seg & 1) * RH, HC >> 2, lw, lane);
+      scale_query(qs, qmul + (seg % QM) * RH, HC >> 3, lw, lane);
       hand_over(q_full);
     };
-    uint8_t* const dst = ks + flip * CH + r0 * 128;
+    uint8_t* const dst = ks + team * 2 * CH + flip * CH + r0 * 128;
 #pragma unroll 1
     for (int g = 0; g < ntile && ok; ++g) {
       if (u == n) {
@@ -1111,37 +1136,33 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         u = 0;
         if (g == 0) query();                         // while its rows are looked up
       }
-      if (!(ok = ok && await(&ku_full[0], g & 1, a.err))) break;
-      const uint8_t* src = smem + L::OFF_KU + r0 * 256 + pc * 16;
+      const uint8_t* raw = smem + L::OFF_KU;
       uint4 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = lds16(src + i * 16 * 256);
 #pragma unroll 1
-      for (int d = 0; d < 4; ++d) {
-        const bool free = mbar_test_wait(&k_empty[d & 1], (d >> 1) ^ 1);
-        if (d & 1) ok = ok && await(&ku_full[(d + 1) >> 1], g & 1, a.err);
-        src += d & 1 ? KUB - 128 : 128;
-        if (u == 0 && g > 0 && d == 2) query();      // both slots are full: their scores wait for the query
-        if (!(ok = ok && (__all_sync(0xffffffffu, free) || await(&k_empty[d & 1], (d >> 1) ^ 1, a.err)))) break;
-        uint8_t* to = dst + (d & 1) * 2 * CH;
+      for (int d = 0; d < 2; ++d) {
+        const int pitch = 256 + 64 * d;
+        const uint8_t* src = raw + d * KUB + r0 * pitch + team * 128 + pc * 16;
+        const bool free = mbar_test_wait(&k_empty[team], d ^ 1);
+        if (u == 0 && g > 0 && d == 1) query();      // both slots are full: their scores wait for the query
+        if (!(ok = ok && await(&ku_full[d], g & 1, a.err))) break;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 c = v[i];
-          if (d < 3) v[i] = lds16(src + i * 16 * 256);
-          else if (i < 2) v[i] = lds16(smem + L::OFF_KU + 2 * KUB + rp * 64 + (lt & 3) * 16 + i * 32 * 64);
-          store_wide(to + i * 16 * 128, 2 * (pc & 3), r0 & 7, flip, c);
+        for (int i = 0; i < 4; ++i) v[i] = lds16(src + i * 16 * pitch);
+        if (!(ok = __all_sync(0xffffffffu, free) || await(&k_empty[team], d ^ 1, a.err))) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_wide(dst + i * 16 * 128, 2 * (pc & 3), r0 & 7, flip, v[i]);
+        hand_over(&k_full[team]);
+        if (team == 0 && d == 1) {
+          if (!(ok = await(&k_empty[2], (g & 1) ^ 1, a.err))) break;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) v[i] = lds16(raw + KUB + (rp + 32 * i) * 320 + 256 + (lt & 3) * 16);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            store_wide(ks + 4 * CH + (rp + 32 * i) * 128, 2 * (lt & 3), rp & 7, 0, v[i]);
+          hand_over(&k_full[2]);
         }
-        hand_over(&k_full[d & 1]);
-        if ((d & 1) && lane == 0) mbar_arrive(&ku_empty[d >> 1]);   // only now: the stores have waited for the loads
+        if (lane == 0) mbar_arrive(&ku_empty[d]);    // only now: the stores have waited for the loads
         __syncwarp();
       }
-      if (!(ok = ok && await(&k_empty[2], (g & 1) ^ 1, a.err))) break;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        store_wide(ks + 4 * CH + (rp + 32 * i) * 128, 2 * (lt & 3), rp & 7, 0, v[i]);
-      hand_over(&k_full[2]);
-      if (lane == 0) mbar_arrive(&ku_empty[2]);
-      __syncwarp();
       ++u;
     }
     // the MMAs have read every key
@@ -1150,7 +1171,8 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   } else if (KV8) {
     // ------------------------------------------------------------ e4m3: values widened
     // A unit at a time.  thread: 16 codes of four tokens, as above.
-    const int lt = (warp - (SMX0 + SMX + GROUP)) * 32 + lane;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    const int lt = (warp - (SMX0 + SMX + 2 * GROUP)) * 32 + lane;
     const int pc = lt & 15, r0 = lt >> 4, flip = (pc >> 2) & 1;
     bool ok = true;
     Ring<VR> vr;
@@ -1351,14 +1373,15 @@ cudaError_t launch_attend(const __nv_bfloat16* q, const void* pool, const float*
   // boxes of several rows are used where the rows are consecutive
   if (kv_scales) {
     const CUtensorMapSwizzle flat = CU_TENSOR_MAP_SWIZZLE_NONE;
+    const CUtensorMapDataType u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
     ok = ok && encode_tiled_2d(&m.row, u8, pool, DSA_DIM, pool_rows, DSA_DIM, 256, 1, flat) &&
          encode_tiled_2d(&m.run, u8, pool, DSA_DIM, pool_rows, DSA_DIM, 256, RUN, flat) &&
-         encode_tiled_2d(&m.row_pos, u8, pool, DSA_DIM, pool_rows, DSA_DIM, 64, 1, flat) &&
-         encode_tiled_2d(&m.run_pos, u8, pool, DSA_DIM, pool_rows, DSA_DIM, 64, RUN, flat);
+         encode_tiled_2d(&m.row_hi, u32, pool, DSA_DIM / 4, pool_rows, DSA_DIM, 80, 1, flat) &&
+         encode_tiled_2d(&m.run_hi, u32, pool, DSA_DIM / 4, pool_rows, DSA_DIM, 80, RUN, flat);
   } else {
     ok = ok && encode_tiled_2d(&m.row, bf, pool, DSA_DIM, pool_rows, DSA_DIM * 2, 64, 1) &&
          encode_chunks_bf16(&m.run, pool, KC, pool_rows, DSA_DIM * 2, 8, 3) &&
-         encode_chunks_bf16(&m.run_pos, pool, KC, pool_rows, DSA_DIM * 2, RUN, 4);
+         encode_chunks_bf16(&m.run_hi, pool, KC, pool_rows, DSA_DIM * 2, RUN, 4);
   }
   if (!ok) return cudaErrorInvalidValue;
   cudaError_t e = idx ? launch<true, true>(a, m, pairs, st)
