@@ -1,5 +1,6 @@
 // Latent-cache append: the rows that the attention calls read are written here,
-// the position part rotated on the way.  Token t of sequence b sits at position p = q_vis[t] - 1 and its row is
+// the position part rotated on the way.  Token t of sequence b sits at position
+// p = q_vis[t] - 1 and its row is
 //   [ kv[t, 0:512] | rot(k_pe[t, 0:64]) ],
 //   rot: (x, y) -> (x cos(a) - y sin(a), y cos(a) + x sin(a)),  a = p * inv_freq[i],
 // with (x, y) = elements (i, i + 32), or (2i, 2i + 1) when interleaved.
@@ -19,6 +20,13 @@
 // share a run hold its rows in registers between the maximum and the rounding,
 // up to four a warp, so a row is read once and all its loads are under way at
 // once; longer runs (blocks of more than 64 tokens) are read twice.
+//
+// Measured: 32,000 tokens of eight prompts into blocks of 64, e4m3: 25.1 us, 2.2 TB/s,
+// 2.9 times its bytes.  Two CTAs fit an SM, since the rows take the registers, so
+// there are two rounds of about 10 us, each a chain of loads (offsets, position,
+// page, rows) and one exchange of the maximum; sending the rows to L2 ahead of the
+// chain made it 27.3 us.  8,000 tokens, bf16: 5.9 us of the GPU's time, 10.9 us with
+// the call.  A single token: 3.7 us of the GPU's, 12 us with the call.
 #include "common.cuh"
 #include "internal.h"
 
