@@ -257,6 +257,20 @@ __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, uint32_t* 
   return true;
 }
 
+// two of them, their answers under way together
+__device__ __forceinline__ bool await_both(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1,
+                                           uint32_t* err) {
+#pragma unroll 1
+  for (uint32_t it = 0;; ++it) {
+    const bool first = try_wait_ns(bar0, parity0), second = try_wait_ns(bar1, parity1);
+    if (__all_sync(0xffffffffu, first && second)) return true;
+    if (it == WAIT_TRIES) {
+      raise_error(err, DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // a ring of N slots: the one in turn, and the parity of its use
 template <int N>
 struct Ring {
@@ -890,10 +904,9 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
 #pragma unroll 1
       for (int u = 0; u < n; ++u, ++g) {
         const uint32_t sb = g & 1, slot = g % RR;
-        if (ok) ok = await(&r_full[slot], (g / RR) & 1, a.err);
-        const uint32_t live = mask[slot * 4 + 2 * hh + cg];
-        if (ok) ok = await(&s_full[sb], (g >> 1) & 1, a.err);
+        if (ok) ok = await_both(&r_full[slot], (g / RR) & 1, &s_full[sb], (g >> 1) & 1, a.err);
         tc_fence_after();
+        const uint32_t live = mask[slot * 4 + 2 * hh + cg];
         float z[32];
         tmem_ld32(lane_base + S_COL + sb * NH + cg * 32, z);
         // the scores are there, so the query's factors are

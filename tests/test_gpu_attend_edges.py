@@ -228,6 +228,17 @@ def test_many_short_queries_repeat_their_bits(heads, e4m3):
     check_attend(first[0][some], first[1][some], ref, e4m3)
 
 
+@pytest.mark.parametrize("heads", [128, 64])
+def test_queries_of_one_tile_each_keep_their_own_factors(heads):
+    """Scores run ahead of the values over several queries: each has a size of its own, so that another's scaling shows."""
+    cache = Cache([120], 64, True, 64, seed=57)
+    Q = 600
+    q = queries(cache, Q, heads).float()
+    q *= torch.exp2(torch.randint(-30, 4, (Q, heads, 1), device=DEV, generator=cache.g).float())
+    vis = ints([(17 * i) % 120 + 1 for i in range(Q)])
+    check_sinks(cache, q.to(torch.bfloat16), cache.offsets([Q]), vis, 0, 120)
+
+
 # ---------------------------------------------------------------------- append
 def test_blocks_longer_than_the_registers_hold():
     """Runs of more than 64 rows are read twice; an old scale that is no power of two, and rows that are not finite."""
