@@ -1121,9 +1121,8 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     // ------------------------------------------------------------ e4m3: keys widened, queries scaled
     // Two chunks at a time, the first and third pair of them by one group of four
     // warps, the second and fourth by another; the positions by the first.  thread:
-    // 16 codes of four tokens; those of the next pair come to registers while these
-    // are widened.  Lanes of odd chunks store their two pieces in the other order,
-    // so that the eight lanes of a store lie in different banks.
+    // 16 codes of four tokens.  Lanes of odd chunks store their two pieces in the
+    // other order, so that the eight lanes of a store lie in different banks.
     if constexpr (KV8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     const int lw = warp - (SMX0 + SMX), team = lw / GROUP;
     const int lt = (lw % GROUP) * 32 + lane;
