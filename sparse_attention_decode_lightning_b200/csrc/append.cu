@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 512, W == 1 ? 1 : 2) latent_app
   __shared__ int n_runs;
   __shared__ float wmax[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();                                     // an attention that follows sets itself up meanwhile
   if (tid == 0) n_runs = 0;
   for (int i = tid; i <= A.B; i += THREADS) off[i] = A.q_offsets[i];
   __syncthreads();

@@ -71,13 +71,15 @@
 // What bounds it.  bf16: a tile takes about 4200 cycles on a pair, its 147 KB from
 // DRAM at a 74th of the copy rate 3100; the rings, all the shared memory there
 // is, hold one tile, so a load's latency is not quite covered.  16 users, 128 heads,
-// windows of 8192: 57.6 us, 2.3 TB/s.  e4m3: about 5300 cycles, of which the MMAs
+// windows of 8192: 55.6 us, 2.4 TB/s.  e4m3: about 5300 cycles, of which the MMAs
 // are 2200; shared memory moves some 4000 cycles' worth a tile (the widening reads 1 and
 // writes 2 bytes a code, MMAs read 4 for it), the softmax is busy for 3600.  4 users,
 // 128 heads, dense over 131072 tokens: 211 us, 691 TFLOP/s, 1.4 TB/s of codes.
-// About 15 us of a launch are not tiles: the shares, the first look-up (three
+// About 13 us of a launch are not tiles: the shares, the first look-up (three
 // dependent loads), cold instructions (the hot code is kept below 60 KB: past the
-// instruction cache every warp slows down several times), output, merge.
+// instruction cache every warp slows down several times), output, merge.  The launch
+// itself, barriers and tensor memory come beside the end of the kernel before
+// (programmatic serialization): one user's selected step 27.0 -> 24.6 us.
 #include "common.cuh"
 #include "internal.h"
 
@@ -507,6 +509,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     mbar_fence_init();
   }
   if (warp == 0) tmem_alloc_pair(tmem_holder, TMEM_COLS);
+  pdl_wait();                                        // so far nothing was read or written that another kernel touches
 
   // This pair's share [t0, t1) of all tiles: a thread sums the tiles of some
   // consecutive queries, the block scans the sums.  Where there is enough of
@@ -1243,6 +1246,7 @@ __global__ void __launch_bounds__(MT, 4) attend_merge_kernel(const int32_t* desc
                                                              float* lse) {
   __shared__ uint4 turn[32][17];
   __shared__ int tails[MAX_PAIRS], heads[MAX_PAIRS];
+  pdl_trigger();
   pdl_wait();
   const int p = blockIdx.x, pairs = gridDim.x;
   if (threadIdx.x < pairs) {
@@ -1334,13 +1338,15 @@ cudaError_t launch(const AttendArgs& a, const AttendMaps& m, int pairs, cudaStre
   cfg.blockDim = dim3(Plan<KV8>::THREADS, 1, 1);
   cfg.dynamicSmemBytes = Plan<KV8>::SMEM_BYTES;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  unsigned int na = 1;
+  add_pdl_attr(attr, &na, true);                     // its barriers and tensor memory beside the end of the kernel before
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = na;
   return cudaLaunchKernelEx(&cfg, kernel, a, m);
 }
 

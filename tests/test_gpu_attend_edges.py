@@ -239,6 +239,65 @@ def test_queries_of_one_tile_each_keep_their_own_factors(heads):
     check_sinks(cache, q.to(torch.bfloat16), cache.offsets([Q]), vis, 0, 120)
 
 
+def test_captured_behind_every_sort_of_node():
+    """A call begins beside the end of the kernel before it: captured after a copy, a memset, a join of two streams, another
+    kernel, an append and itself, with one workspace, it still reads what those wrote."""
+    cache = Cache([3000, 70], 64, True, 64, seed=58)
+    off, vis = cache.offsets([1, 1]), ints([3000, 70])
+    f, ws = inv_freq(), dsa.attend_workspace(128)
+    q, other = queries(cache, 2, 128), queries(cache, 2, 128)
+    row = torch.randn(2, D, device=DEV, generator=cache.g).to(torch.bfloat16)
+    host = queries(cache, 2, 128).cpu().pin_memory()
+    outs = [(torch.empty(2, 128, DV, dtype=torch.bfloat16, device=DEV), torch.empty(2, 128, device=DEV)) for _ in range(6)]
+
+    def attend(i):
+        dsa.dsa_mla_decode_sinks(q, cache.pool, cache.table, off, vis, 2, 1, 2900, SCALE, *outs[i], ws, kv_scales=cache.scales)
+
+    def steps(stream, side):
+        attend(0)
+        attend(1)                                                  # behind the call's own merge
+        q.copy_(host, non_blocking=True)                           # a copy node
+        attend(2)
+        q.zero_()
+        attend(3)
+        side.wait_stream(stream)                                   # a join of two streams
+        with torch.cuda.stream(side):
+            q.copy_(other)
+        row.mul_(1.5)
+        stream.wait_stream(side)
+        attend(4)
+        dsa.dsa_latent_append(row[:, :DV], row[:, DV:], f, cache.pool, cache.table, off, vis, 2, ws, kv_scales=cache.scales)
+        attend(5)
+
+    stream, side = torch.cuda.Stream(), torch.cuda.Stream()
+    kept = [t.clone() for t in (q, row, cache.pool, cache.scales)]
+    results = []
+    for how in ("eager", "graph"):
+        for t, k in zip((q, row, cache.pool, cache.scales), kept):
+            t.copy_(k)
+        torch.cuda.synchronize()
+        if how == "eager":
+            with torch.cuda.stream(stream):
+                for _ in range(2):
+                    steps(stream, side)
+                    stream.synchronize()
+                    results.append([t.clone() for o in outs for t in o])
+        else:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=stream):
+                steps(stream, side)
+            for _ in range(2):
+                graph.replay()
+                torch.cuda.synchronize()
+                results.append([t.clone() for o in outs for t in o])
+    dsa.dsa_check_error(ws)
+    for i in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(results[i], results[2 + i]))
+    zero = results[0][2 * 3]
+    assert torch.equal(results[0][0], results[0][2]) and not torch.equal(results[0][4], results[0][2])
+    assert not torch.equal(zero, results[0][4]) and not torch.equal(results[0][8], results[0][10])
+
+
 # ---------------------------------------------------------------------- append
 def test_blocks_longer_than_the_registers_hold():
     """Runs of more than 64 rows are read twice; an old scale that is no power of two, and rows that are not finite."""
