@@ -368,11 +368,12 @@ size_t dsa_attend_workspace_bytes(int heads);
  * rows that the set does not hold are not read.
  * Precision: products accumulate in fp32 on the tensor cores; scores, maxima
  * and sums are fp32.  Over a bf16 cache the softmax weights are rounded to
- * bf16 for the value product; over an e4m3 cache weights, codes and queries
- * are fp16 there (codes exactly; weights times their block's scale, so that
- * the largest of a head is at least 1 over the largest scale's block, and one
- * 2^-14 of that has still 11 bits; queries after scaling each head by a power of
- * two, exact except for elements 2^-28 times smaller than the head's largest).
+ * bf16 for the value product.  Over an e4m3 cache codes, weights and queries
+ * are fp16 there.  Codes are exact.  A weight enters times its block's scale and
+ * keeps 11 bits where that product is at least 2^-21 of the head's largest one;
+ * below, its bits fade, and from 2^-32 down the token is missing from O (LSE
+ * counts it).  Queries are scaled head by head by a power of two, exact except
+ * for elements 2^-28 times smaller than the head's largest.
  * Rows that no sequence holds (before q_offsets[0], from q_offsets[B] on) are
  * left as they were, whatever their q_vis.
  * ws: at least dsa_attend_workspace_bytes(heads) bytes, 16-byte aligned.

@@ -27,13 +27,15 @@
 // weight, is the size of the output's own).  e4m3 cache: codes widened to fp16
 // (exact), q scaled by a power of two a head so that its largest element lies
 // in [2^14, 2^15) and rounded to fp16 (exact for all that is not 2^-28 times
-// smaller), P as fp16.  The scales enter in fp32.  A tile whose scales lie within
-// a factor of 2^15 has one, its largest s, and its tokens factors f_j = s_j / s:
-// with z_j = q . code_j f_j s + log2 s, P_j = exp2(z_j - m) f_j <= 2^8 and
-// l = sum exp2(z_j - m) / s.  Another tile takes s_j for s and f_j = 1.  m is
-// the running maximum of z, log2 s included, so that P fits whatever the scales
-// are; P's smallest normal value is 2^-14, and down to there it keeps 11 bits.
-// Sums, maxima and O are fp32.
+// smaller), P as fp16.  The scales enter in fp32, token by token: with
+//   z_j = log2(e) scale q . code_j s_j + log2 s_j,
+//   P_j = 2^(z_j - m + 7) = weight_j s_j 2^7 / 2^m,   l = sum P_j / s_j,
+// O = P code / l.  m follows the largest z, that is the largest product of a weight
+// and its scale, and may lag by 8: that token's P lies in [2^7, 2^15], fp16's upper
+// end.  Another's keeps 11 bits down to 2^-14, so as long as weight x scale is at
+// least 2^-21 of the largest, and is lost below 2^-32 of it.  (One scale a tile, its
+// largest, with factors s_j / s in P, saves an addition but lost every weight of a
+// tile in which another token's scale is much larger.)  Sums, maxima and O are fp32.
 //
 // Tensor memory (512 columns): O [0,256), lanes 0..63 dims 0..255 of the CTA's
 // heads, lanes 64..127 dims 256..511 | scores slot 0 [256,320) | slot 1
@@ -127,9 +129,8 @@ struct Plan {
   static constexpr int OFF_P = OFF_V + VR * VSLOT;   // [2][64 heads x 64 tokens]
   static constexpr int OFF_KU = OFF_P + 2 * CH;      // e4m3: units of a tile's keys
   static constexpr int OFF_VU = OFF_KU + (KV8 ? NH * DSA_DIM : 0);
-  static constexpr int OFF_SCL = OFF_VU + (KV8 ? VUR * VUB : 0);       // e4m3: float [RR][128]: scale of each token, over the tile's where it has one
-  static constexpr int OFF_TILE = OFF_SCL + (KV8 ? RR * NT * 4 : 0);  // float4 [RR]: scale, log2, 1 / scale of the tile; w: it has one
-  static constexpr int OFF_ROWS = OFF_TILE + (KV8 ? RR * 16 : 0);      // int32 [RR][128]: pool row or -1
+  static constexpr int OFF_SCL = OFF_VU + (KV8 ? VUR * VUB : 0);       // e4m3: float [RR][3][128]: of each token scale x the scores' factor, log2 and 1 / scale
+  static constexpr int OFF_ROWS = OFF_SCL + (KV8 ? RR * 3 * NT * 4 : 0);      // int32 [RR][128]: pool row or -1
   static constexpr int OFF_MASK = OFF_ROWS + RR * NT * 4;            // uint32 [RR][4]: tokens that count
   static constexpr int OFF_RUNS = OFF_MASK + RR * 4 * 4;             // uint32 [4]: bit i: rows 16 i .. 16 i + 15 are consecutive, or none is held
   static constexpr int OFF_QMUL = OFF_RUNS + 16;                     // float [QM][64], by segment
@@ -449,7 +450,6 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   uint8_t* vs = smem + L::OFF_V;
   uint8_t* ps = smem + L::OFF_P;
   float* scl = reinterpret_cast<float*>(smem + L::OFF_SCL);
-  float4* tsc = reinterpret_cast<float4*>(smem + L::OFF_TILE);
   int* rows = reinterpret_cast<int*>(smem + L::OFF_ROWS);
   uint32_t* mask = reinterpret_cast<uint32_t*>(smem + L::OFF_MASK);
   uint32_t* runs = reinterpret_cast<uint32_t*>(smem + L::OFF_RUNS);
@@ -784,29 +784,18 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         const uint32_t g = i - 3, slot = g % RR;
         if (!(ok = await(&r_empty[slot], ((g / RR) & 1) ^ 1, a.err))) break;
         if constexpr (KV8) {
-          // A tile has one scale, its largest, where the others are at least
-          // 2^-15 of it, so that P times their ratio stays within fp16; other tiles
-          // keep one a token.
-          uint32_t lo = 0xffffffffu, hi = 0;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (row[k] >= 0 && !(s[k] >= 0x1p-40f && s[k] <= 0x1p40f)) {
               row[k] = -1;
               bad = true;
             }
-            if (row[k] >= 0) {
-              lo = min(lo, __float_as_uint(s[k]));
-              hi = max(hi, __float_as_uint(s[k]));
-            }
+            const float st = row[k] < 0 ? 1.f : s[k];
+            float* sc = scl + slot * 3 * NT + 32 * k + lane;
+            sc[0] = st * a.scale_log2;
+            sc[NT] = log2f(st);
+            sc[2 * NT] = __fdiv_rn(1.f, st);
           }
-          lo = __reduce_min_sync(0xffffffffu, lo);
-          hi = __reduce_max_sync(0xffffffffu, hi);
-          const float st = hi == 0 ? 1.f : __uint_as_float(hi), inv = __fdiv_rn(1.f, st);
-          const bool one = hi == 0 || __uint_as_float(lo) >= st * 0x1p-15f;
-          if (lane == 0) tsc[slot] = make_float4(st * a.scale_log2, log2f(st), inv, one ? 1.f : 0.f);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            scl[slot * NT + 32 * k + lane] = row[k] < 0 ? 1.f : one ? s[k] * inv : s[k];
         }
         uint32_t run = 0;
 #pragma unroll
@@ -894,6 +883,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     const int h = half * HC + r;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t row_bar = 1 + (quarter & 1);      // the four warps of the same rows
+    constexpr float RAISE = KV8 ? 7.f : 0.f;         // P = 2^(z - m + RAISE)
     bool ok = true;
     int q = q0, off = off0, left = r < HC ? ntile : 0;
     uint32_t g = 0;
@@ -920,28 +910,20 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         if (lane == 0) mbar_arrive_pair(leader(&s_empty[sb]));
         __syncwarp();
         float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        float4 ts = make_float4(a.scale_log2, 0.f, 1.f, 1.f);
-        if constexpr (KV8) ts = tsc[slot];
-        const bool one = !KV8 || ts.w != 0.f;
-        const float* sc = scl + slot * NT + hh * NH + cg * 32;
-        if (one) {
-          const float k = ts.x * qm;
-          if constexpr (KV8) {
+        const float* sc = scl + slot * 3 * NT + hh * NH + cg * 32;
+        if constexpr (KV8) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(sc + j);
-              z[j] = fmaf(z[j] * f.x, k, ts.y);
-              z[j + 1] = fmaf(z[j + 1] * f.y, k, ts.y);
-              z[j + 2] = fmaf(z[j + 2] * f.z, k, ts.y);
-              z[j + 3] = fmaf(z[j + 3] * f.w, k, ts.y);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) z[j] *= k;
+          for (int j = 0; j < 32; j += 4) {
+            const float4 k = *reinterpret_cast<const float4*>(sc + j);
+            const float4 e = *reinterpret_cast<const float4*>(sc + NT + j);
+            z[j] = fmaf(z[j] * k.x, qm, e.x);
+            z[j + 1] = fmaf(z[j + 1] * k.y, qm, e.y);
+            z[j + 2] = fmaf(z[j + 2] * k.z, qm, e.z);
+            z[j + 3] = fmaf(z[j + 3] * k.w, qm, e.w);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) z[j] = fmaf(z[j] * qm, sc[j] * a.scale_log2, __log2f(sc[j]));
+          for (int j = 0; j < 32; ++j) z[j] *= a.scale_log2;
         }
         if (live != 0xffffffffu) {
 #pragma unroll
@@ -954,8 +936,8 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         mxs[(2 * hh + cg) * RH] = mtile;
         named_barrier(row_bar, 128);
         mtile = fmaxf(fmaxf(mxs[0], mxs[RH]), fmaxf(mxs[2 * RH], mxs[3 * RH]));
-        // the maximum that P refers to moves only when it falls 8 behind (a
-        // factor of 2^8, which fp16 holds), so O is seldom rescaled
+        // the maximum that P refers to moves only when it falls 8 behind, so O is
+        // seldom rescaled; with RAISE P reaches 2^15, which fp16 holds
         float alpha = 1.f;
         bool resc = false;
         if (mtile > m_use + 8.f) {
@@ -965,29 +947,24 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
           }
           m_use = mtile;
         }
-        const float m_eff = m_use == -INFINITY ? 0.f : m_use;
+        const float m_eff = m_use == -INFINITY ? 0.f : m_use - RAISE;
         float sums[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < 32; ++j) z[j] = fast_exp2(z[j] - m_eff);
-        if (one) {
+        if constexpr (KV8) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sums[j & 3] += z[j];
-          if constexpr (KV8) {
-            // the values are codes: P takes their scales, over the tile's
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(sc + j);
-              z[j] *= f.x;
-              z[j + 1] *= f.y;
-              z[j + 2] *= f.z;
-              z[j + 3] *= f.w;
-            }
+          for (int j = 0; j < 32; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(sc + 2 * NT + j);
+            sums[0] = fmaf(z[j], f.x, sums[0]);
+            sums[1] = fmaf(z[j + 1], f.y, sums[1]);
+            sums[2] = fmaf(z[j + 2], f.z, sums[2]);
+            sums[3] = fmaf(z[j + 3], f.w, sums[3]);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) sums[j & 3] += __fdividef(z[j], sc[j]);
+          for (int j = 0; j < 32; ++j) sums[j & 3] += z[j];
         }
-        l = fmaf(l, alpha, ((sums[0] + sums[1]) + (sums[2] + sums[3])) * (KV8 && one ? ts.z : 1.f));
+        l = fmaf(l, alpha, (sums[0] + sums[1]) + (sums[2] + sums[3]));
         // the value MMAs of the tile before have read P and written O
         if (ok && g > 0) ok = await(pv_done, (g - 1) & 1, a.err);
         uint8_t* pr = ps + hh * CH + r * 128;
@@ -1070,7 +1047,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       }
       if (hh == 0 && cg == 0 && mine)
         (whole ? a.lse + static_cast<size_t>(q) * a.H + h : a.l_part + static_cast<size_t>(part) * a.H + h)[0] =
-            none ? -INFINITY : (m_use + log2f(l)) * 0.69314718055994531f;
+            none ? -INFINITY : (m_use - RAISE + log2f(l)) * 0.69314718055994531f;
       tc_fence_before();                             // O was read before the next segment writes it
     }
     if (half == 0 && warp == SMX0 && lane == 0 && ntile > 0) {
