@@ -6,6 +6,7 @@ and raises DSAError on a non-zero status.  No step of the computation runs in
 Python, and there is no fallback: if libdsa.so is missing, loading fails.
 """
 import ctypes
+import operator
 import os
 from typing import Optional, Sequence
 
@@ -295,6 +296,15 @@ def _ws_at(ws: torch.Tensor, dev: int):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _tokens(name: str, n) -> int:
+    """A count of tokens as the C call's int, which keeps the lower 32 bits of a larger one: no context is
+    longer than its largest value."""
+    n = operator.index(n)
+    if n < 0:
+        raise ValueError(f"{name}: expected 0 or more, got {n}")
+    return n if n < 0x7FFFFFFF else 0x7FFFFFFF
+
+
 def _raw_stream(stream, dev: int) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
@@ -366,8 +376,9 @@ def attend_workspace(heads: int = HEADS, device="cuda") -> torch.Tensor:
 def dsa_mla_decode_sinks(q, kv_pool, page_table, q_offsets, q_vis, B, sinks, window, scale, out,
                          lse, ws, kv_scales=None, stream=None):
     """MLA decode over the first `sinks` and the last `window` visible tokens, of a
-    bf16 cache or (kv_scales) a block-scaled e4m3 one; out bf16 [Q,heads,512],
-    lse fp32 [Q,heads]; see include/dsa.h."""
+    bf16 cache or (kv_scales) a block-scaled e4m3 one; a window of any size at least
+    the context is dense attention.  out bf16 [Q,heads,512], lse fp32 [Q,heads]; see
+    include/dsa.h."""
     dev = _device_of(q)
     if q.dim() != 3:
         raise ValueError("q: [Q, heads, 576]")
@@ -376,8 +387,8 @@ def dsa_mla_decode_sinks(q, kv_pool, page_table, q_offsets, q_vis, B, sinks, win
                                                                               q_vis, Q, B, dev)
     p_ws, n_ws = _ws_at(ws, dev)
     status = (_lib or lib()).dsa_mla_decode_sinks(
-        _at("q", q, _BF16, (Q, H, DIM), dev), pool, scales, pages, page, block, table, max_pages, off, vis, B, Q, H, sinks,
-        window, scale, _at("out", out, _BF16, (Q, H, DIM_V), dev), _at("lse", lse, _F32, (Q, H), dev), p_ws, n_ws,
+        _at("q", q, _BF16, (Q, H, DIM), dev), pool, scales, pages, page, block, table, max_pages, off, vis, B, Q, H,
+        _tokens("sinks", sinks), _tokens("window", window), scale, _at("out", out, _BF16, (Q, H, DIM_V), dev), _at("lse", lse, _F32, (Q, H), dev), p_ws, n_ws,
         _raw_stream(stream, dev))
     if status:
         raise DSAError(status, "dsa_mla_decode_sinks")

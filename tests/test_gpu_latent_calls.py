@@ -1,0 +1,30 @@
+"""Calls of the latent cache's operators that the argument lists allow: counts beyond 32 bits."""
+import math
+
+import pytest
+import torch
+
+import sparse_attention_decode_lightning_b200 as dsa
+from tests._latent import D, DV, Cache
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+SCALE = 192 ** -0.5
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("sinks,window", [(0, 1 << 32), (0, 1 << 40), (0, (1 << 63) - 1), (1 << 40, 0), (1 << 32, 1 << 32)])
+def test_a_count_beyond_32_bits_is_dense_attention(e4m3, sinks, window):
+    lens = [700, 1, 129]
+    cache = Cache(lens, 64, e4m3, 16, seed=3)
+    q = torch.randn(3, 128, D, device=DEV, generator=cache.g).to(torch.bfloat16)
+    off, vis = cache.offsets([1] * 3), torch.tensor(lens, dtype=torch.int32, device=DEV)
+    ws = dsa.attend_workspace(128)
+    results = []
+    for s, w in ((0, 700), (sinks, window)):
+        out = torch.full((3, 128, DV), math.nan, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((3, 128), math.nan, device=DEV)
+        dsa.dsa_mla_decode_sinks(q, cache.pool, cache.table, off, vis, 3, s, w, SCALE, out, lse, ws, kv_scales=cache.scales)
+        results.append((out, lse))
+    dsa.dsa_check_error(ws)
+    assert torch.equal(results[0][0], results[1][0]) and torch.equal(results[0][1], results[1][1])
