@@ -331,7 +331,8 @@ dsa_status dsa_sparse_mla_decode_fp8(const void* q, const void* kv_pool, float k
  * outside every sequence, and cache rows of other positions, stay as they
  * were.  A page that is appended to belongs to one sequence of the call.
  * B <= DSA_MAX_BATCH; T, and the rows of a sequence, are not limited.
- * ws: at least 256 bytes (the error word).
+ * ws: at least 256 bytes (the error word).  ws and the arrays of 32-bit words may
+ * lie on any 4-byte boundary, here and in the two calls below (their ws: 16).
  */
 dsa_status dsa_latent_append(const void* kv, int64_t ld_kv, const void* k_pe, int64_t ld_pe,
                              const float* inv_freq, int interleaved, const int32_t* page_table,

@@ -27,6 +27,7 @@ struct NvtxRange {
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
 
@@ -529,10 +530,10 @@ static dsa_status cache_checks(const void* kv_pool, const float* kv_scales, int 
                                int page_size, int scale_block, const int32_t* page_table,
                                int max_pages) {
   if (!kv_pool || !page_table || num_pages <= 0 || max_pages <= 0) return DSA_ERR_INVALID_ARG;
-  if (!aligned16(kv_pool)) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(kv_pool) || !aligned4(page_table)) return DSA_ERR_INVALID_ARG;
   if (!page_size_ok(page_size, num_pages)) return DSA_ERR_UNSUPPORTED;
   if (kv_scales) {
-    if (reinterpret_cast<uintptr_t>(kv_scales) & 3u) return DSA_ERR_INVALID_ARG;
+    if (!aligned4(kv_scales)) return DSA_ERR_INVALID_ARG;
     if (scale_block < 1 || (scale_block & (scale_block - 1)) || scale_block > page_size)
       return DSA_ERR_UNSUPPORTED;
   }
@@ -547,7 +548,8 @@ dsa_status dsa_latent_append(const void* kv, int64_t ld_kv, const void* k_pe, in
   if (!kv || !k_pe || !inv_freq || !q_offsets || !q_vis || !ws) return DSA_ERR_INVALID_ARG;
   if (B <= 0 || T <= 0) return DSA_ERR_INVALID_ARG;
   if (ld_kv < DSA_DIM_V || (ld_kv & 7) || !aligned16(kv)) return DSA_ERR_INVALID_ARG;
-  if (ld_pe < DSA_DIM - DSA_DIM_V || (ld_pe & 1) || (reinterpret_cast<uintptr_t>(k_pe) & 3u))
+  if (ld_pe < DSA_DIM - DSA_DIM_V || (ld_pe & 1) || !aligned4(k_pe)) return DSA_ERR_INVALID_ARG;
+  if (!aligned4(inv_freq) || !aligned4(q_offsets) || !aligned4(q_vis) || !aligned4(ws))
     return DSA_ERR_INVALID_ARG;
   dsa_status s = cache_checks(kv_pool, kv_scales, num_pages, page_size, scale_block, page_table,
                               max_pages);
@@ -571,6 +573,7 @@ static dsa_status attend_checks(const void* q, const int32_t* q_offsets, const i
   if (!q || !q_offsets || !q_vis || !out || !lse || !ws) return DSA_ERR_INVALID_ARG;
   if (B <= 0 || Q <= 0) return DSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return DSA_ERR_INVALID_ARG;
+  if (!aligned4(q_offsets) || !aligned4(q_vis) || !aligned4(lse)) return DSA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || scale > 3.0e38f) return DSA_ERR_INVALID_ARG;
   if (!heads_ok(heads)) return DSA_ERR_UNSUPPORTED;
   if (B > DSA_MAX_BATCH || Q > 65535) return DSA_ERR_UNSUPPORTED;
@@ -604,7 +607,7 @@ dsa_status dsa_sparse_mla_decode_fp8_block(const void* q, const void* kv_pool,
                                            const int32_t* q_vis, const int32_t* idx, int B, int Q,
                                            int heads, int topk, float scale, void* out, float* lse,
                                            void* ws, size_t ws_bytes, void* stream) {
-  if (!kv_scales || !idx || topk <= 0) return DSA_ERR_INVALID_ARG;
+  if (!kv_scales || !idx || !aligned4(idx) || topk <= 0) return DSA_ERR_INVALID_ARG;
   dsa_status s = cache_checks(kv_pool, kv_scales, num_pages, page_size, scale_block, page_table,
                               max_pages);
   if (s != DSA_OK) return s;
