@@ -327,7 +327,8 @@ dsa_status dsa_sparse_mla_decode_fp8(const void* q, const void* kv_pool, float k
  * padding and is skipped, the first row of a sequence only where all are; any
  * other row that breaks the order, and a position without a valid page, is
  * skipped and flagged (DSA_ERR_DEVICE_BOUNDS), as is a partly filled block's
- * old scale outside [2^-40, 2^40] (its codes are left as they are).  Rows
+ * old scale outside [2^-40, 2^40] (its codes are left as they are), and a
+ * sequence whose offsets leave [0, T], all of which is skipped.  Rows
  * outside every sequence, and cache rows of other positions, stay as they
  * were.  A page that is appended to belongs to one sequence of the call.
  * B <= DSA_MAX_BATCH; T, and the rows of a sequence, are not limited.

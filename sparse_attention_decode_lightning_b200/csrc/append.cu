@@ -195,7 +195,10 @@ __device__ __forceinline__ Run find_run(const AppendArgs& A, const int* off, int
     if (off[mid] <= t) lo = mid; else hi = mid;
   }
   const int f = off[lo];
-  if (f < 0 || f > t || off[lo + 1] > A.T) return r;
+  if (f < 0 || f > t || off[lo + 1] > A.T) {              // offsets that are none: nothing is known of their rows
+    raise_error(A.err, DEVERR_BOUNDS);
+    return r;
+  }
   const int v0 = A.q_vis[f];
   const int v = A.q_vis[t];
   if (v0 <= 0) {                                          // a padded sequence
