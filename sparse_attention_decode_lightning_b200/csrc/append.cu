@@ -16,12 +16,19 @@
 // fraction of 2^64; p times that wraps as the angle does, and its upper half is
 // the angle to 2^-32 of a turn.
 //
-// Bound: bytes (1152 read, 576 or 1152 written a token).  The sixteen warps that
-// share a run hold its rows in registers between the maximum and the rounding,
-// up to four a warp, so a row is read once and all its loads are under way at
-// once; longer runs (blocks of more than 64 tokens) are read twice.
+// Bound: bytes (1152 read, 576 or 1152 written a token).  A run, the new rows of one
+// block, is short, up to four rows, which one warp takes, or long, which all warps of
+// the CTA share.  The kernel made for the sort that the batch has more of holds its
+// rows in registers between the maximum and the rounding, up to four a warp, so a row
+// is read once and all its loads are under way at once; rows of the other sort, and of
+// blocks of more than 64 tokens, are read twice.
 //
-// Measured: 32,000 tokens of eight prompts into blocks of 64, e4m3: 25.1 us, 2.2 TB/s,
+// Mixed batches (us of the GPU's time, blocks of 64): 512 single tokens 7.1, a chunk of
+// 1024 9.8, both in one call 14.3; 64 single tokens 4.0, eight chunks of 4000 20.8, both
+// 20.8.  One warp a run, or all warps a run, for the whole batch by its average length
+// took 45.8 and 82.8.
+//
+// Measured: 32,000 tokens of eight prompts into blocks of 64, e4m3: 24.7 us, 2.3 TB/s,
 // 2.9 times its bytes.  Two CTAs fit an SM, since the rows take the registers, so
 // there are two rounds of about 10 us, each a chain of loads (offsets, position,
 // page, rows) and one exchange of the maximum; sending the rows to L2 ahead of the
@@ -227,144 +234,164 @@ __device__ __forceinline__ Run find_run(const AppendArgs& A, const int* off, int
   return r;
 }
 
-// W warps a run: 1 of a CTA's 8 where runs are short (decode, small blocks), all
-// 16 where they are long.
-template <bool KV8, int W>
-__global__ void __launch_bounds__(W == 1 ? 256 : 512, W == 1 ? 1 : 2) latent_append_kernel(const __grid_constant__ AppendArgs A) {
-  constexpr int WARPS = W == 1 ? 8 : W, THREADS = 32 * WARPS;
+// The rows of a run, bf16 cache: as they are, the position part rotated; by one warp
+__device__ __forceinline__ void append_bf16(const AppendArgs& A, const Run& r, const Freq& freq, int lane) {
+  for (int i = 0; i < r.n; ++i) {
+    const int v = A.q_vis[r.t + i];
+    if (v != r.vis0 + i) {
+      if (v != 0 && lane == 0) raise_error(A.err, DEVERR_BOUNDS);
+      continue;
+    }
+    Row w = load_row(A, r.t + i, lane);
+    rotate(w, r.pos + i, freq);
+    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(A.pool) + (r.slot + i) * DSA_DIM;
+    reinterpret_cast<uint4*>(dst)[2 * lane] = w.a;
+    reinterpret_cast<uint4*>(dst)[2 * lane + 1] = w.b;
+    dst[DSA_DIM_V + (A.interleaved ? 2 * lane : lane)] = __float2bfloat16_rn(w.x);
+    dst[DSA_DIM_V + (A.interleaved ? 2 * lane + 1 : lane + 32)] = __float2bfloat16_rn(w.y);
+  }
+}
+
+// The rows of a run, e4m3 cache, by W warps (1, or all of the CTA's, which then meet
+// at barriers): this is warp wg of them.  HOLD: a warp holds up to KEEP rows in
+// registers between the maximum and the rounding; else, and where there are more,
+// they are read twice.  wmax: a word for each of the W.
+template <int W, bool HOLD>
+__device__ __forceinline__ void append_e4m3(const AppendArgs& A, const Run& r, const Freq& freq, int wg, int lane, float* wmax) {
+  const int held = r.pos & ((1 << A.block_shift) - 1);       // tokens the block holds already
+  float* sp = A.scales + (r.slot >> A.block_shift);
+  const float old = held ? *sp : 0.f;
+  float m = 0.f;
+  bool any = false;
+  Row keep[KEEP];
+  uint32_t kept = 0, odd = 0;                                // rows in registers; of them not finite in this lane
+  const bool held_back = HOLD && (W == 1 || r.n <= KEEP * W);   // every row stays in registers; one warp takes no more
+  if (held_back) {
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) {
+      const int i = wg + j * W;
+      if (i >= r.n) break;
+      const int v = A.q_vis[r.t + i];
+      if (v == r.vis0 + i) {
+        kept |= 1u << j;
+        keep[j] = load_row(A, r.t + i, lane);
+      } else if (v != 0 && lane == 0) {
+        raise_error(A.err, DEVERR_BOUNDS);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j)
+      if (kept >> j & 1u) {
+        rotate(keep[j], r.pos + wg + j * W, freq);
+        bool finite;
+        m = fmaxf(m, lane_amax(keep[j], &finite));
+        odd |= finite ? 0u : 1u << j;
+      }
+    any = kept != 0;
+  } else {
+    for (int i = wg; i < r.n; i += W) {
+      const int v = A.q_vis[r.t + i];
+      if (v != r.vis0 + i) {
+        if (v != 0 && lane == 0) raise_error(A.err, DEVERR_BOUNDS);
+        continue;
+      }
+      any = true;
+      Row w = load_row(A, r.t + i, lane);
+      rotate(w, r.pos + i, freq);
+      bool finite;
+      m = fmaxf(m, lane_amax(w, &finite));
+    }
+  }
+  m = warp_max(m);
+  if constexpr (W > 1) {
+    if (lane == 0) wmax[wg] = any ? m : -1.f;
+    __syncthreads();
+    m = -1.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) m = fmaxf(m, wmax[i]);
+    any = m >= 0.f;
+    __syncthreads();                                         // wmax is free, every thread holds `old`
+  }
+  if (!any) return;                                          // nothing but padding
+  float s = exp2f(static_cast<float>(needed_exp(m)));
+  const bool old_ok = old >= 0x1p-40f && old <= 0x1p40f;
+  if (held && !old_ok && lane == 0 && wg == 0) raise_error(A.err, DEVERR_BOUNDS);
+  if (held && old_ok) s = fmaxf(s, old);
+  __syncwarp();
+  if (lane == 0 && wg == 0) *sp = s;
+  if (held && old_ok && s > old) {
+    const float ratio = __fdiv_rn(old, s);
+    uint4* base = reinterpret_cast<uint4*>(A.pool + (r.slot - held) * DSA_DIM);
+    for (int i = wg * 32 + lane; i < held * (DSA_DIM / 16); i += 32 * W) {
+      uint4 c = base[i];
+      c = make_uint4(rescale4(c.x, ratio), rescale4(c.y, ratio), rescale4(c.z, ratio), rescale4(c.w, ratio));
+      base[i] = c;
+    }
+  }
+  const float inv = __fdiv_rn(1.f, s);                       // exact where s is a power of two; an old scale may be none
+  const bool exact = (__float_as_uint(s) & 0x7FFFFFu) == 0;
+  if (held_back && exact) {
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j)
+      if (kept >> j & 1u) store_e4m3(A, r.slot + wg + j * W, keep[j], inv, !(odd >> j & 1u), lane);
+  } else {
+    for (int i = wg; i < r.n; i += W) {
+      if (A.q_vis[r.t + i] != r.vis0 + i) continue;
+      Row w = load_row(A, r.t + i, lane);
+      rotate(w, r.pos + i, freq);
+      if (exact) {
+        bool finite;
+        lane_amax(w, &finite);
+        store_e4m3(A, r.slot + i, w, inv, finite, lane);
+      } else {
+        uint8_t* dst = A.pool + (r.slot + i) * DSA_DIM;
+        reinterpret_cast<uint4*>(dst)[lane] = make_uint4(f8_div4(w.a.x, w.a.y, s), f8_div4(w.a.z, w.a.w, s),
+                                                         f8_div4(w.b.x, w.b.y, s), f8_div4(w.b.z, w.b.w, s));
+        dst[DSA_DIM_V + (A.interleaved ? 2 * lane : lane)] = static_cast<uint8_t>(f8(__fdiv_rn(w.x, s)));
+        dst[DSA_DIM_V + (A.interleaved ? 2 * lane + 1 : lane + 32)] = static_cast<uint8_t>(f8(__fdiv_rn(w.y, s)));
+      }
+    }
+  }
+}
+
+// A CTA takes the runs that start in its G rows: short ones (decode, verify steps,
+// small blocks) a warp each, long ones with all warps together, whatever the batch
+// mixes.  LONG: made for long runs, whose rows its 16 warps hold, 64 registers a
+// thread; else for short ones (bf16: runs of one row), which a warp holds alone.  The
+// other sort's rows are read twice, so that they take no registers from the first.
+template <bool KV8, bool LONG>
+__global__ void __launch_bounds__(LONG ? 512 : 256, LONG ? 2 : 1) latent_append_kernel(const __grid_constant__ AppendArgs A) {
+  constexpr int WARPS = LONG ? 16 : 8, THREADS = 32 * WARPS;
   __shared__ int off[DSA_MAX_BATCH + 1];
-  __shared__ Run runs[MAX_G];
-  __shared__ int n_runs;
+  __shared__ Run runs[MAX_G];                        // short ones from the front, long ones from the end
+  __shared__ int n_short, n_long;
   __shared__ float wmax[WARPS];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();                                     // an attention that follows sets itself up meanwhile
-  if (tid == 0) n_runs = 0;
+  if (tid == 0) n_short = n_long = 0;
   for (int i = tid; i <= A.B; i += THREADS) off[i] = A.q_offsets[i];
   __syncthreads();
   if (tid < A.G) {
     const int64_t t = static_cast<int64_t>(blockIdx.x) * A.G + tid;
     if (t < A.T) {
       const Run r = find_run(A, off, static_cast<int>(t));
-      if (r.n > 0) runs[atomicAdd(&n_runs, 1)] = r;       // any order: runs are independent
+      if (r.n > KEEP) runs[MAX_G - 1 - atomicAdd(&n_long, 1)] = r;   // any order: runs are independent
+      else if (r.n > 0) runs[atomicAdd(&n_short, 1)] = r;
     }
   }
   __syncthreads();
   const Freq freq = turns_of(A.inv_freq[lane]);
-  constexpr int GROUPS = WARPS / W;
-  const int group = warp / W, wg = warp % W;
-  for (int k = group; k < n_runs; k += GROUPS) {
-    const Run r = runs[k];
-    if constexpr (!KV8) {
-      for (int i = wg; i < r.n; i += W) {
-        const int v = A.q_vis[r.t + i];
-        if (v != r.vis0 + i) {
-          if (v != 0 && lane == 0) raise_error(A.err, DEVERR_BOUNDS);
-          continue;
-        }
-        Row w = load_row(A, r.t + i, lane);
-        rotate(w, r.pos + i, freq);
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(A.pool) + (r.slot + i) * DSA_DIM;
-        reinterpret_cast<uint4*>(dst)[2 * lane] = w.a;
-        reinterpret_cast<uint4*>(dst)[2 * lane + 1] = w.b;
-        dst[DSA_DIM_V + (A.interleaved ? 2 * lane : lane)] = __float2bfloat16_rn(w.x);
-        dst[DSA_DIM_V + (A.interleaved ? 2 * lane + 1 : lane + 32)] = __float2bfloat16_rn(w.y);
-      }
-    } else {
-      const int held = r.pos & ((1 << A.block_shift) - 1);   // tokens the block holds already
-      float* sp = A.scales + (r.slot >> A.block_shift);
-      const float old = held ? *sp : 0.f;
-      float m = 0.f;
-      bool any = false;
-      Row keep[KEEP];
-      uint32_t kept = 0, odd = 0;                          // rows in registers; of them not finite in this lane
-      const bool held_back = r.n <= KEEP * W;              // every row stays in registers
-      if (held_back) {
-#pragma unroll
-        for (int j = 0; j < KEEP; ++j) {
-          const int i = wg + j * W;
-          if (i >= r.n) break;
-          const int v = A.q_vis[r.t + i];
-          if (v == r.vis0 + i) {
-            kept |= 1u << j;
-            keep[j] = load_row(A, r.t + i, lane);
-          } else if (v != 0 && lane == 0) {
-            raise_error(A.err, DEVERR_BOUNDS);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < KEEP; ++j)
-          if (kept >> j & 1u) {
-            rotate(keep[j], r.pos + wg + j * W, freq);
-            bool finite;
-            m = fmaxf(m, lane_amax(keep[j], &finite));
-            odd |= finite ? 0u : 1u << j;
-          }
-        any = kept != 0;
-      } else {
-        for (int i = wg; i < r.n; i += W) {
-          const int v = A.q_vis[r.t + i];
-          if (v != r.vis0 + i) {
-            if (v != 0 && lane == 0) raise_error(A.err, DEVERR_BOUNDS);
-            continue;
-          }
-          any = true;
-          Row w = load_row(A, r.t + i, lane);
-          rotate(w, r.pos + i, freq);
-          bool finite;
-          m = fmaxf(m, lane_amax(w, &finite));
-        }
-      }
-      m = warp_max(m);
-      if constexpr (W > 1) {
-        if (lane == 0) wmax[warp] = any ? m : -1.f;
-        __syncthreads();
-        m = -1.f;
-#pragma unroll
-        for (int i = 0; i < WARPS; ++i) m = fmaxf(m, wmax[i]);
-        any = m >= 0.f;
-        __syncthreads();                                   // wmax is free, every thread holds `old`
-      }
-      if (!any) continue;                                  // nothing but padding
-      float s = exp2f(static_cast<float>(needed_exp(m)));
-      const bool old_ok = old >= 0x1p-40f && old <= 0x1p40f;
-      if (held && !old_ok && lane == 0 && wg == 0) raise_error(A.err, DEVERR_BOUNDS);
-      if (held && old_ok) s = fmaxf(s, old);
-      __syncwarp();
-      if (lane == 0 && wg == 0) *sp = s;
-      if (held && old_ok && s > old) {
-        const float ratio = __fdiv_rn(old, s);
-        uint4* base = reinterpret_cast<uint4*>(A.pool + (r.slot - held) * DSA_DIM);
-        for (int i = wg * 32 + lane; i < held * (DSA_DIM / 16); i += 32 * W) {
-          uint4 c = base[i];
-          c = make_uint4(rescale4(c.x, ratio), rescale4(c.y, ratio), rescale4(c.z, ratio), rescale4(c.w, ratio));
-          base[i] = c;
-        }
-      }
-      const float inv = __fdiv_rn(1.f, s);                 // exact where s is a power of two; an old scale may be none
-      const bool exact = (__float_as_uint(s) & 0x7FFFFFu) == 0;
-      if (held_back && exact) {
-#pragma unroll
-        for (int j = 0; j < KEEP; ++j)
-          if (kept >> j & 1u) store_e4m3(A, r.slot + wg + j * W, keep[j], inv, !(odd >> j & 1u), lane);
-      } else {
-        for (int i = wg; i < r.n; i += W) {
-          if (A.q_vis[r.t + i] != r.vis0 + i) continue;
-          Row w = load_row(A, r.t + i, lane);
-          rotate(w, r.pos + i, freq);
-          if (exact) {
-            bool finite;
-            lane_amax(w, &finite);
-            store_e4m3(A, r.slot + i, w, inv, finite, lane);
-          } else {
-            uint8_t* dst = A.pool + (r.slot + i) * DSA_DIM;
-            reinterpret_cast<uint4*>(dst)[lane] = make_uint4(f8_div4(w.a.x, w.a.y, s), f8_div4(w.a.z, w.a.w, s),
-                                                             f8_div4(w.b.x, w.b.y, s), f8_div4(w.b.z, w.b.w, s));
-            dst[DSA_DIM_V + (A.interleaved ? 2 * lane : lane)] = static_cast<uint8_t>(f8(__fdiv_rn(w.x, s)));
-            dst[DSA_DIM_V + (A.interleaved ? 2 * lane + 1 : lane + 32)] = static_cast<uint8_t>(f8(__fdiv_rn(w.y, s)));
-          }
-        }
-      }
+  if constexpr (KV8) {
+    for (int k = MAX_G - 1; k > MAX_G - 1 - n_long; --k) {
+      const Run r = runs[k];
+      append_e4m3<WARPS, LONG>(A, r, freq, warp, lane, wmax);
     }
+    for (int k = warp; k < n_short; k += WARPS) {
+      const Run r = runs[k];
+      append_e4m3<1, !LONG>(A, r, freq, 0, lane, nullptr);
+    }
+  } else {
+    for (int k = warp; k < n_short; k += WARPS) append_bf16(A, runs[k], freq, lane);
   }
 }
 
@@ -399,15 +426,11 @@ cudaError_t launch_latent_append(const __nv_bfloat16* kv, int64_t ld_kv, const _
   const int fill = 4 * device_sm_count();
   A.G = T / fill < 1 ? 1 : (T / fill > MAX_G ? MAX_G : T / fill);
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(T) + A.G - 1) / A.G);
-  if (!scales) {
-    latent_append_kernel<false, 1><<<grid, 256, 0, st>>>(A);
-  } else {
-    // rows a run can have: a warp takes short runs alone
-    const int per_seq = (T + B - 1) / B;
-    const int rows = per_seq < scale_block ? per_seq : scale_block;
-    if (rows <= 4) latent_append_kernel<true, 1><<<grid, 256, 0, st>>>(A);
-    else latent_append_kernel<true, 16><<<grid, 512, 0, st>>>(A);
-  }
+  // The average rows a sequence say which sort of runs the batch has more of; either
+  // kernel takes both.
+  if (!scales) latent_append_kernel<false, false><<<grid, 256, 0, st>>>(A);
+  else if (T <= static_cast<int64_t>(KEEP) * B || scale_block <= KEEP) latent_append_kernel<true, false><<<grid, 256, 0, st>>>(A);
+  else latent_append_kernel<true, true><<<grid, 512, 0, st>>>(A);
   return cudaGetLastError();
 }
 
