@@ -378,6 +378,11 @@ size_t dsa_attend_workspace_bytes(int heads);
  * for elements 2^-28 times smaller than the head's largest.
  * Rows that no sequence holds (before q_offsets[0], from q_offsets[B] on) are
  * left as they were, whatever their q_vis.
+ * Stream order: the kernel is launched with programmatic stream serialization and
+ * reads and writes nothing before it has waited for the kernel ahead of it on the
+ * stream.  A caller's kernel there that has that attribute too must execute
+ * griddepcontrol.wait itself, or what is older may still run; other kernels,
+ * copies and this library's calls need nothing.
  * ws: at least dsa_attend_workspace_bytes(heads) bytes, 16-byte aligned.
  */
 dsa_status dsa_mla_decode_sinks(const void* q, const void* kv_pool, const float* kv_scales,

@@ -135,7 +135,7 @@ struct Plan {
   static constexpr int OFF_RUNS = OFF_MASK + RR * 4 * 4;             // uint32 [4]: bit i: rows 16 i .. 16 i + 15 are consecutive, or none is held
   static constexpr int OFF_QMUL = OFF_RUNS + 16;                     // float [QM][64], by segment
   static constexpr int OFF_MX = OFF_QMUL + QM * RH * 4;              // float [2][4][64]: between the parts of a row
-  static constexpr int OFF_SCAN = OFF_MX + 8 * RH * 4;               // int64 [28]; the share's first and last tile; its first query and that one's tile
+  static constexpr int OFF_SCAN = OFF_MX + 8 * RH * 4;               // int64 [28]; the share's first and last tile; its first query, and that one's tile and tiles
   static constexpr int OFF_BAR = OFF_SCAN + 32 * 8;
   static constexpr int NBAR = 2 * RR + 2 * KS + 2 * VR + 4 + 4 + (KV8 ? 1 + 2 * KU + 2 * VUR : 0);
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
@@ -192,13 +192,13 @@ struct List {
 
 // whether a sequence holds query q; the results of others stay as they were
 __device__ __forceinline__ bool held(const AttendArgs& a, int q) {
-  const int first = __ldg(a.q_offsets), end = __ldg(a.q_offsets + a.B);
+  const int first = a.q_offsets[0], end = a.q_offsets[a.B];
   return (q >= first) & (q < end);
 }
 
-__device__ __forceinline__ int visible(const AttendArgs& a, int q) {
-  const int seen = __ldg(a.q_vis + q);               // in flight beside the offsets
-  const int v = held(a, q) ? max(0, seen) : 0;
+// tokens it attends to, of `seen` visible ones: those that its pages can hold
+__device__ __forceinline__ int visible(const AttendArgs& a, bool mine, int seen) {
+  const int v = mine ? max(0, seen) : 0;
   const int64_t cap = static_cast<int64_t>(a.max_pages) << a.page_shift;
   return v < cap ? v : static_cast<int>(cap);
 }
@@ -217,7 +217,8 @@ __device__ __forceinline__ List list_of(const AttendArgs& a, int vis) {
 template <bool IDX>
 __device__ __noinline__ int tiles_of(const AttendArgs& a, int q) {
   if constexpr (IDX) return (a.topk + NT - 1) / NT;
-  return max(1u, (list_of(a, visible(a, q)).n + NT - 1) / NT);
+  const int seen = a.q_vis[q];                       // in flight beside the offsets
+  return max(1u, (list_of(a, visible(a, held(a, q), seen)).n + NT - 1) / NT);
 }
 
 __device__ __forceinline__ int seq_of_query(const int32_t* q_offsets, int B, int q, int lane) {
@@ -225,7 +226,7 @@ __device__ __forceinline__ int seq_of_query(const int32_t* q_offsets, int B, int
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
     const int i = lo + lane * step;
-    const uint32_t m = __ballot_sync(0xffffffffu, i < hi && __ldg(q_offsets + i) <= q);
+    const uint32_t m = __ballot_sync(0xffffffffu, i < hi && q_offsets[i] <= q);
     if (m == 0) break;                     // q lies before the first sequence
     lo += (31 - __clz(m)) * step;
     hi = min(hi, lo + step);
@@ -477,6 +478,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   uint64_t* vu_full = ku_empty + KU;       // e4m3: [2] units of value codes
   uint64_t* vu_empty = vu_full + VUR;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::OFF_MISC);
+  int* held_rows = reinterpret_cast<int*>(tmem_holder + 1);   // [2] the sequences' first query, and one past the last
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int half = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -509,7 +511,10 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     mbar_fence_init();
   }
   if (warp == 0) tmem_alloc_pair(tmem_holder, TMEM_COLS);
-  pdl_wait();                                        // so far nothing was read or written that another kernel touches
+  // So far nothing was read or written that another kernel touches.  What is read from
+  // here on may have been written beside the lines above, by an append or a selector,
+  // so these are plain loads, not those for data that stays constant while a kernel lives.
+  pdl_wait();
 
   // This pair's share [t0, t1) of all tiles: a thread sums the tiles of some
   // consecutive queries, the block scans the sums.  Where there is enough of
@@ -526,7 +531,10 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     if (lane >= o) incl += v;
   }
   if (lane == 31) scan[warp] = incl;
-  if (tid < 2) scan[28 + tid] = 0;
+  if (tid < 2) {
+    scan[28 + tid] = 0;
+    held_rows[tid] = a.q_offsets[tid * a.B];
+  }
   __syncthreads();
   int64_t before = lane < THREADS / 32 ? scan[lane] : 0;
 #pragma unroll 1
@@ -553,9 +561,9 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       const int64_t at_cost = base + static_cast<int64_t>(start) * qa;
       if (c >= at_cost && c < at_cost + sum + static_cast<int64_t>(start) * (qb - qa)) {
         int64_t left = c - at_cost;
-        int q = qa;
+        int q = qa, n;
 #pragma unroll 1
-        for (int n; left >= start + (n = tiles_of<IDX>(a, q)); ++q) {
+        for (; left >= start + (n = tiles_of<IDX>(a, q)); ++q) {
           left -= start + n;
           at += n;
         }
@@ -563,13 +571,23 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         scan[28 + i] = at + off;
         if (i == 0) {
           scan[30] = q;
-          scan[31] = off;
+          scan[31] = off | static_cast<int64_t>(n) << 32;
         }
       }
     }
   }
   tc_fence_before();
-  cluster_sync();                                    // both CTAs' barriers and tensor memory are there
+  __syncwarp();
+  cluster_arrive();
+  __syncthreads();                                   // the share is known
+  // its first query's loads, while the other CTA arrives
+  int seen0 = 0, seq0 = 0;
+  if (warp == 3 && scan[29] > scan[28]) {
+    seen0 = a.q_vis[scan[30]];
+    seq0 = seq_of_query(a.q_offsets, a.B, static_cast<int>(scan[30]), lane);
+  }
+  __syncwarp();
+  cluster_wait();                                    // both CTAs' barriers and tensor memory are there
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const int q0 = static_cast<int>(scan[30]);
@@ -577,6 +595,12 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   const int ntile = static_cast<int>(scan[29] - scan[28]);
   if (half == 0 && tid < 2 && ntile == 0) a.desc[2 * pair + tid] = -1;
 
+  // the tiles of the share's first query are known already
+  auto tiles = [&](int q) {
+    if constexpr (!IDX)
+      if (q == q0) return static_cast<int>(scan[31] >> 32);
+    return tiles_of<IDX>(a, q);
+  };
   // the first CTA's barrier of the same name
   auto leader = [&](uint64_t* bar) { return map_to_rank(smem_u32(bar), 0); };
   // a warp's part of an operand is written: tell the MMA issuer
@@ -619,7 +643,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     uint32_t g = 0;                              // tiles so far
 #pragma unroll 1
     for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
-      const int n = min(tiles_of<IDX>(a, q) - off, left);
+      const int n = min(tiles(q) - off, left);
       left -= n;
       if (!(ok = await(q_full, seg & 1, a.err))) break;
 #pragma unroll 1
@@ -662,7 +686,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     if (ntile > 0) load_query(q, 0, lead);
 #pragma unroll 1
     for (uint32_t seg = 0; left > 0 && ok; ++seg, ++q, off = 0) {
-      const int n = min(tiles_of<IDX>(a, q) - off, left);
+      const int n = min(tiles(q) - off, left);
       left -= n;
 #pragma unroll 1
       for (int u = 0; u < n && ok; ++u, ++g) {
@@ -827,7 +851,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         row[k] = -1;
         if (pg[k] >= 0 && pg[k] < a.num_pages) row[k] = (pg[k] << a.page_shift) + (at[k] & ((1 << a.page_shift) - 1));
         bad |= at[k] >= 0 && row[k] < 0;
-        if constexpr (KV8) s[k] = row[k] >= 0 ? __ldg(a.kv_scales + (row[k] >> a.block_shift)) : 1.f;
+        if constexpr (KV8) s[k] = row[k] >= 0 ? a.kv_scales[row[k] >> a.block_shift] : 1.f;
         // The row on its way to L2, half a row a CTA: it is loaded about two tiles
         // from now, which a load from DRAM would not quite fit into.
         if (row[k] >= 0) {
@@ -841,19 +865,22 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       for (int k = 0; k < 4; ++k) {
         at[k] = pos[k] >= 0 && pos[k] < vis1 ? pos[k] : -1;
         bad |= at[k] != pos[k] && pos[k] != -1 && vis1 >= 0;
-        pg[k] = at[k] >= 0 ? __ldg(pages1 + (at[k] >> a.page_shift)) : -1;
+        pg[k] = at[k] >= 0 ? pages1[at[k] >> a.page_shift] : -1;
       }
       if (i < ntile && u == n) {
         ++q;
         off = i == 0 ? off0 : 0;
-        n = min(tiles_of<IDX>(a, q) - off, left);
+        n = min(tiles(q) - off, left);
         left -= n;
         u = 0;
-        pages = a.page_table + static_cast<size_t>(seq_of_query(a.q_offsets, a.B, q, lane)) * a.max_pages;
-        vis = visible(a, q);
+        const int seen = i == 0 ? seen0 : a.q_vis[q];   // in flight beside the search
+        const int seq = i == 0 ? seq0 : seq_of_query(a.q_offsets, a.B, q, lane);
+        const bool mine = q >= held_rows[0] && q < held_rows[1];
+        pages = a.page_table + static_cast<size_t>(seq) * a.max_pages;
+        vis = visible(a, mine, seen);
         ls = list_of(a, vis);
-        if (!held(a, q)) vis = -1;                   // nothing is read, and no index is a fault
-        else bad |= __ldg(a.q_vis + q) > vis;
+        if (!mine) vis = -1;                         // nothing is read, and no index is a fault
+        else bad |= seen > vis;
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -861,7 +888,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         pos[k] = -1;
         if (i < ntile) {
           if constexpr (IDX) {
-            if (j < static_cast<uint32_t>(a.topk)) pos[k] = __ldg(a.idx + static_cast<size_t>(q) * a.topk + j);
+            if (j < static_cast<uint32_t>(a.topk)) pos[k] = a.idx[static_cast<size_t>(q) * a.topk + j];
           } else {
             pos[k] = ls.position(j);
           }
@@ -890,7 +917,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     int head_q = -1, tail_q = -1;                    // queries this pair holds a part of
 #pragma unroll 1
     for (uint32_t seg = 0; left > 0; ++seg, ++q, off = 0) {
-      const int nt = tiles_of<IDX>(a, q);
+      const int nt = tiles(q);
       const int n = min(nt - off, left);
       left -= n;
       float qm = 1.f, m_use = -INFINITY, l = 0.f;
@@ -1005,7 +1032,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
       const bool whole = n == nt;
       const bool head = off == 0;
       const int part = 2 * pair + (head ? 1 : 0);
-      const bool mine = held(a, q);
+      const bool mine = q >= held_rows[0] && q < held_rows[1];
       if (!whole && mine) (head ? head_q : tail_q) = q;
       const float inv = l > 0.f || l != l ? 1.f / l : 0.f;   // NaN stays NaN
       const bool none = l == 0.f;
@@ -1071,7 +1098,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     Ring<VR> vr;
 #pragma unroll 1
     for (; left > 0 && ok; ++q, off = 0) {
-      const int n = min(tiles_of<IDX>(a, q) - off, left);
+      const int n = min(tiles(q) - off, left);
       left -= n;
 #pragma unroll 1
       for (int u = 0; u < n && ok; ++u, ++g) {
@@ -1124,7 +1151,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
           ++seg;
           off = 0;
         }
-        n = min(tiles_of<IDX>(a, q) - off, left);
+        n = min(tiles(q) - off, left);
         left -= n;
         u = 0;
         if (g == 0) query();                         // while its rows are looked up

@@ -156,9 +156,13 @@ cudaError_t launch_attend(const __nv_bfloat16* q, const void* pool, const float*
                           float scale, __nv_bfloat16* out, float* lse, void* ws, cudaStream_t st);
 
 // pdl = true: the kernel may start before the previous kernel on the stream
-// ends (programmatic dependent launch); it waits for it in pdl_wait().  Only
-// set where the previous kernel is one of this library's, launched by the same
-// entry point, so everything older on the stream has finished before it.
+// ends (programmatic dependent launch); it waits for it in pdl_wait().  Reads
+// before pdl_wait() are allowed only where the previous kernel is launched by the
+// same entry point.  Everything older on the stream has finished after pdl_wait()
+// if the previous kernel itself began, or waited, behind it: kernels launched
+// without the attribute begin behind it, those of this library that have it call
+// pdl_wait().  launch_attend() sets it behind whatever the stream holds, and
+// dsa.h asks the same of a caller's own kernels.
 inline void add_pdl_attr(cudaLaunchAttribute* attrs, unsigned int* n, bool pdl) {
   if (!pdl) return;
   attrs[*n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
