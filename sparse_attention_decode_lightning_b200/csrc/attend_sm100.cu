@@ -142,6 +142,10 @@ struct Plan {
   static constexpr int SMEM_BYTES = OFF_MISC + 16;
   static_assert(SMEM_BYTES <= 232448, "shared memory exceeds the sm_100 limit");
   static_assert(WARPS <= 28, "scan");
+  static_assert(OFF_K % 1024 == 0 && OFF_V % 1024 == 0 && OFF_P % 1024 == 0, "atoms of the swizzle");
+  static_assert(OFF_KU % 128 == 0 && KUB % 128 == 0 && OFF_VU % 128 == 0, "TMA boxes");
+  static_assert(OFF_SCL % 16 == 0 && OFF_ROWS % 16 == 0, "16-byte reads");
+  static_assert(OFF_SCAN % 8 == 0 && OFF_BAR % 8 == 0, "64-bit words and barriers");
 };
 constexpr uint32_t O_COL = 0, S_COL = 256, TMEM_COLS = 512;
 
@@ -235,9 +239,11 @@ __device__ __forceinline__ int seq_of_query(const int32_t* q_offsets, int B, int
 }
 
 // Waits of a whole warp for the phase of the given parity, bounded by their
-// number of tries (about two seconds).  A try suspends the warp for up to
-// WAIT_NS, so that it leaves the issue slots to others: polled barriers took half of
-// all slots.  The limit bounds how late an arrival from the peer CTA is seen.
+// number of tries: 2^22 of at most 200 ns and some 100 cycles each, about one second.
+// A try suspends the warp for up to WAIT_NS, so that it leaves the issue slots to
+// others: polled barriers took half of all slots.  WAIT_NS bounds how late an arrival
+// from the peer CTA is seen.  A wait that gives up does so a second after the copies
+// that were issued before it, so they have landed when its warp ends.
 constexpr uint32_t WAIT_TRIES = 1u << 22, WAIT_NS = 200;
 __device__ __forceinline__ bool try_wait_ns(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
@@ -319,7 +325,12 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
 // Arrive on a barrier of the cluster (its address there) after this CTA's own
 // shared-memory writes, which the fence before has made the tensor core's.  At
 // the default scope: a release at cluster scope (mbar_arrive_remote) waits for
-// every access under way, 1300 to 2000 cycles here
+// every access under way, 1300 to 2000 cycles here.  That CTA scope is enough is an
+// assumption: the other CTA's warp that waits for it reads none of the data, it issues
+// MMAs, and this SM's tensor core reads this SM's shared memory, where the fence has
+// put the writes.
+// The lane that arrives leaves its branch by a __syncwarp: the tcgen05, cluster and
+// named barrier instructions behind it are undefined for a warp that is not whole.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -359,8 +370,8 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// four e4m3 codes -> four fp16, exactly.  Written in PTX: the intrinsic of the
-// pair type costs twice the instructions.
+// four e4m3 codes -> four fp16, exactly.  Written in PTX: with the intrinsic of the
+// pair type a warp took 800 cycles for its part of a raw unit, with this 479.
 __device__ __forceinline__ uint2 widen4(uint32_t w) {
   uint2 r;
   asm("{\n\t.reg .b16 lo, hi;\n\t"
@@ -510,7 +521,10 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
     mbar_init(bars + i, n);
     mbar_fence_init();
   }
-  if (warp == 0) tmem_alloc_pair(tmem_holder, TMEM_COLS);
+  if (warp == 0) {
+    __syncwarp();                                    // the allocation wants its warp whole
+    tmem_alloc_pair(tmem_holder, TMEM_COLS);
+  }
   // So far nothing was read or written that another kernel touches.  What is read from
   // here on may have been written beside the lines above, by an append or a selector,
   // so these are plain loads, not those for data that stays constant while a kernel lives.
@@ -1005,6 +1019,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
           *reinterpret_cast<uint4*>(pr + (((4 * cg + j) ^ (r & 7)) << 4)) = w;
         }
         if (__any_sync(0xffffffffu, resc)) {
+          __syncwarp();
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
