@@ -225,19 +225,6 @@ __device__ __noinline__ int tiles_of(const AttendArgs& a, int q) {
   return max(1u, (list_of(a, visible(a, held(a, q), seen)).n + NT - 1) / NT);
 }
 
-__device__ __forceinline__ int seq_of_query(const int32_t* q_offsets, int B, int q, int lane) {
-  int lo = 0, hi = B;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + lane * step;
-    const uint32_t m = __ballot_sync(0xffffffffu, i < hi && q_offsets[i] <= q);
-    if (m == 0) break;                     // q lies before the first sequence
-    lo += (31 - __clz(m)) * step;
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
 // Waits of a whole warp for the phase of the given parity, bounded by their
 // number of tries: 2^22 of at most 200 ns and some 100 cycles each, about one second.
 // A try suspends the warp for up to WAIT_NS, so that it leaves the issue slots to
@@ -598,7 +585,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
   int seen0 = 0, seq0 = 0;
   if (warp == 3 && scan[29] > scan[28]) {
     seen0 = a.q_vis[scan[30]];
-    seq0 = seq_of_query(a.q_offsets, a.B, static_cast<int>(scan[30]), lane);
+    seq0 = seq_of_query_warp(a.q_offsets, a.B, static_cast<int>(scan[30]), lane);
   }
   __syncwarp();
   cluster_wait();                                    // both CTAs' barriers and tensor memory are there
@@ -888,7 +875,7 @@ __global__ void __launch_bounds__(Plan<KV8>::THREADS, 1)
         left -= n;
         u = 0;
         const int seen = i == 0 ? seen0 : a.q_vis[q];   // in flight beside the search
-        const int seq = i == 0 ? seq0 : seq_of_query(a.q_offsets, a.B, q, lane);
+        const int seq = i == 0 ? seq0 : seq_of_query_warp(a.q_offsets, a.B, q, lane);
         const bool mine = q >= held_rows[0] && q < held_rows[1];
         pages = a.page_table + static_cast<size_t>(seq) * a.max_pages;
         vis = visible(a, mine, seen);

@@ -537,6 +537,22 @@ __device__ __forceinline__ uint64_t umma_desc_sw128_mn(uint32_t saddr, uint32_t 
   return umma_desc_sw128(saddr, sbo_bytes, lbo_bytes);
 }
 
+// Sequence of query q: the largest b < B with q_offsets[b] <= q (0 where q lies before
+// the first sequence), found by a full warp in rounds of 32 parallel probes (one round
+// for B <= 32, three for B = 2048) instead of a chain of dependent loads.
+__device__ __forceinline__ int seq_of_query_warp(const int32_t* q_offsets, int B, int q, int lane) {
+  int lo = 0, hi = B;                  // the answer lies in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + lane * step;
+    const uint32_t m = __ballot_sync(0xffffffffu, i < hi && q_offsets[i] <= q);
+    if (m == 0) break;                 // lane 0 probes lo: only before the first sequence
+    lo += (31 - __clz(m)) * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
 // ------------------------------------------------------------------ programmatic dependent launch
 // A kernel launched with the programmatic-serialization attribute may start
 // while the previous kernel on the stream is still running; it must call

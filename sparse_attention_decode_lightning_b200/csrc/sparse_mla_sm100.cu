@@ -123,23 +123,6 @@ struct MlaTcArgs {
   uint32_t* err;
 };
 
-// Sequence of query q: the largest b < B with q_offsets[b] <= q, found by a
-// full warp in rounds of 32 parallel probes (one round for B <= 32, three
-// for B = 2048) instead of a chain of dependent loads.
-__device__ __forceinline__ int seq_of_query_warp(const int32_t* q_offsets, int B, int q, int lane) {
-  int lo = 0, hi = B;                  // q_offsets[lo] <= q; the answer lies in [lo, hi)
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + lane * step;
-    const uint32_t m = __ballot_sync(0xffffffffu, i < hi && __ldg(q_offsets + i) <= q);
-    lo += (31 - __clz(m)) * step;      // lane 0 probes lo itself, so m != 0
-    hi = min(hi, lo + step);
-  }
-  return lo;
-}
-
-
-
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint32_t* err) {
   const bool ok = mbar_wait(bar, parity, err);
   return __all_sync(0xffffffffu, ok);
