@@ -33,7 +33,7 @@
 // there are two rounds of about 10 us, each a chain of loads (offsets, position,
 // page, rows) and one exchange of the maximum; sending the rows to L2 ahead of the
 // chain made it 27.3 us.  8,000 tokens, bf16: 5.9 us of the GPU's time, 10.9 us with
-// the call.  A single token: 3.7 us of the GPU's, 12 us with the call.
+// the call.  A single token: 3.2 us of the GPU's, 12 us with the call.
 #include "common.cuh"
 #include "internal.h"
 

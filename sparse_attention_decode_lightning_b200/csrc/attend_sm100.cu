@@ -73,14 +73,16 @@
 // What bounds it.  bf16: a tile takes about 4200 cycles on a pair, its 147 KB from
 // DRAM at a 74th of the copy rate 3100; the rings, all the shared memory there
 // is, hold one tile, so a load's latency is not quite covered.  16 users, 128 heads,
-// windows of 8192: 55.6 us, 2.4 TB/s.  e4m3: about 5300 cycles, of which the MMAs
+// windows of 8192: 56.1 us, 2.4 TB/s.  e4m3: about 5300 cycles, of which the MMAs
 // are 2200; shared memory moves some 4000 cycles' worth a tile (the widening reads 1 and
 // writes 2 bytes a code, MMAs read 4 for it), the softmax is busy for 3600.  4 users,
-// 128 heads, dense over 131072 tokens: 211 us, 691 TFLOP/s, 1.4 TB/s of codes.
-// About 13 us of a launch are not tiles: the shares, the first look-up (three
-// dependent loads), cold instructions (the hot code is kept below 60 KB: past the
-// instruction cache every warp slows down several times), output, merge.  The launch
-// itself, barriers and tensor memory come beside the end of the kernel before
+// 128 heads, dense over 131072 tokens: 213 us, 685 TFLOP/s, 1.4 TB/s of codes.
+// What a call takes beside its tiles, from a fit over 2 to 16 tiles on every pair (a
+// query a pair, replayed as a graph): 11.2 us + 2.4 a tile over bf16, 14.7 + 3.1 over
+// e4m3 (64 heads: 9.4 and 13.5), and 2 more where a query is divided: the shares, the
+// first look-up (three dependent loads), cold instructions (the hot code is kept below
+// 60 KB: past the instruction cache every warp slows down several times), output, merge.
+// The launch itself, barriers and tensor memory come beside the end of the kernel before
 // (programmatic serialization): one user's selected step 27.0 -> 24.6 us.
 #include "common.cuh"
 #include "internal.h"
